@@ -41,30 +41,30 @@ def _rope(name, B, L, H, d, grid, start, dt, pairing, norm, v):
 def listed():
     return [
         # the last norm of a step that works on one token, fp32 modulation: latency
-        _norm("norm, one token", 1, 1, 5120, 1, "bf16", "fp32", "bf16", "layer", False, True),
+        _norm("norm one token", 1, 1, 5120, 1, "bf16", "fp32", "bf16", "layer", False, True),
         # the norm before attention at the Wan-like length: 21 x 45 x 80 tokens of 40 heads of 128
-        _norm("norm, video", 1, 75600, 5120, 1, "bf16", "fp32", "bf16", "layer", False, True),
+        _norm("norm video", 1, 75600, 5120, 1, "bf16", "fp32", "bf16", "layer", False, True),
         # a modulation of its own for each of 13 frames of 391 tokens, batch of 2 (guidance), RMS norm
-        _norm("norm, frames", 2, 13 * 391, 1544, 13, "fp16", "fp16", "fp16", "rms", True, True),
+        _norm("norm frames", 2, 13 * 391, 1544, 13, "fp16", "fp16", "fp16", "rms", True, True),
         # between two blocks, residual stream in fp32, Wan-like length
-        _gate("gate, video", 1, 75600, 5120, 1, "fp32", "bf16", "fp32", "bf16", "layer", False, True, True, "none", 1.0),
+        _gate("gate video", 1, 75600, 5120, 1, "fp32", "bf16", "fp32", "bf16", "layer", False, True, True, "none", 1.0),
         # sandwich norm with an odd width, so that no row but the first is aligned
-        _gate("gate, odd width", 2, 1031, 1285, 1, "bf16", "bf16", "bf16", "bf16", "rms", True, True, True, "rms", 0.5),
+        _gate("gate odd width", 2, 1031, 1285, 1, "bf16", "bf16", "bf16", "bf16", "rms", True, True, True, "rms", 0.5),
         # a single frame's pooled token: latency
-        _rope("rope, one token", 1, 1, 40, 128, "21x45x80", 3600, "bf16", "interleaved", "token", True),
+        _rope("rope one token", 1, 1, 40, 128, "21x45x80", 3600, "bf16", "interleaved", "token", True),
         # the Wan-like projection: query/key norm over the whole width, three axes
-        _rope("rope, video", 1, 75600, 40, 128, "21x45x80", 0, "bf16", "interleaved", "token", True),
+        _rope("rope video", 1, 75600, 40, 128, "21x45x80", 0, "bf16", "interleaved", "token", True),
         # image and text tokens in one sequence, positions given for each token, per-head norm, halves paired
-        _rope("rope, positions", 2, 4096 + 77, 16, 64, "", 0, "fp16", "half", "head", True),
+        _rope("rope positions", 2, 4096 + 77, 16, 64, "", 0, "fp16", "half", "head", True),
         # the modulation's own projection of two guidance branches: six vectors of 5120
-        {"name": "linear, two rows", "op": "linear", "M": 2, "N": 6 * 5120, "K": 5120, "bias": True, "h": "fp32"},
+        {"name": "linear two rows", "op": "linear", "M": 2, "N": 6 * 5120, "K": 5120, "bias": True, "h": "fp32"},
         # q, k and v of the Wan-like length
-        {"name": "linear, video", "op": "linear", "M": 75600, "N": 3 * 5120, "K": 5120, "bias": True, "h": "bf16"},
+        {"name": "linear video", "op": "linear", "M": 75600, "N": 3 * 5120, "K": 5120, "bias": True, "h": "bf16"},
         # a small latent with an odd number of tokens and odd widths, from the norm to the projection
-        {"name": "normlinear, ragged", "op": "normlinear", "B": 2, "L": 517, "C": 1000, "N": 1543, "x": "bf16",
+        {"name": "normlinear ragged", "op": "normlinear", "B": 2, "L": 517, "C": 1000, "N": 1543, "x": "bf16",
          "kind": "layer", "bias": True, "h": "bf16"},
         # the output projection behind 8 heads over 16384 tokens
-        {"name": "attnlinear, image", "op": "attnlinear", "B": 1, "L": 16384, "H": 8, "d": 128, "N": 1024,
+        {"name": "attnlinear image", "op": "attnlinear", "B": 1, "L": 16384, "H": 8, "d": 128, "N": 1024,
          "x": "bf16", "bias": True, "h": "bf16"},
     ]
 
