@@ -20,7 +20,8 @@ __all__ = [
     "FLAG_SELECT_ALL", "FLAG_EXACT_ONLY", "FLAG_SYNC_CHECK", "FLAG_TEST_STALL", "FLAG_FIRST_ORDER", "SolAttnError", "lib", "lib_path",
     "forward", "stats", "forward_host", "stage_pool", "stage_threshold", "stage_fused",
     "workspace_bytes", "release", "kernels_per_forward", "DebugBuffers", "EXPORTED_SYMBOLS", "topk_route",
-    "executed_flops", "BLOCK",
+    "executed_flops", "BLOCK", "norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope",
+    "rope_axes",
 ]
 
 FLAG_SELECT_ALL = 0x1
@@ -42,7 +43,7 @@ EXPORTED_SYMBOLS = (
     "sol_attn_stage_pool", "sol_attn_stage_threshold", "sol_attn_stage_fused",
     "sol_attn_workspace_bytes", "sol_attn_release", "sol_attn_error_string",
     "sol_attn_kernels_per_forward", "sol_attn_forward_noalloc", "sol_attn_profile_read",
-    "sol_attn_noalloc_status", "sol_attn_topk_route",
+    "sol_attn_noalloc_status", "sol_attn_topk_route", "sol_attn_norm_modulate", "sol_attn_rope",
 )
 
 
@@ -89,10 +90,12 @@ def lib():
     L.sol_attn_profile_read.argtypes = [vp, i, i]
     L.sol_attn_noalloc_status.argtypes = [vp]
     L.sol_attn_topk_route.argtypes = [i, i, i, i, i, i, vp, vp]
+    L.sol_attn_norm_modulate.argtypes = [vp, vp]
+    L.sol_attn_rope.argtypes = [vp, vp]
     for name in ("sol_attn_forward", "sol_attn_forward_ex", "sol_attn_stats", "sol_attn_forward_host",
                  "sol_attn_stage_pool", "sol_attn_stage_threshold", "sol_attn_stage_fused", "sol_attn_release",
                  "sol_attn_kernels_per_forward", "sol_attn_forward_noalloc", "sol_attn_profile_read",
-                 "sol_attn_noalloc_status", "sol_attn_topk_route"):
+                 "sol_attn_noalloc_status", "sol_attn_topk_route", "sol_attn_norm_modulate", "sol_attn_rope"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -279,3 +282,15 @@ def executed_flops(selected_pairs: int, B: int, H: int, L: int, d: int, *, appro
     proxy = 4.0 * BLOCK * d * N * N * B * H if approx else 0.0
     route = 2.0 * d * N * N * B * H
     return exact + proxy + route
+
+
+# The operators around the attention import torch, which this module does only where it is used.
+_LAYER_OPS = ("norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes")
+
+
+def __getattr__(name):
+    if name in _LAYER_OPS:
+        from . import layer
+        globals().update({op: getattr(layer, op) for op in _LAYER_OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -9,15 +9,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libsol_attn.so")
 PROFILE_LIB = os.path.join(PKG, "libsol_attn_profile.so")
-SOURCES = [os.path.join(PKG, "csrc", "sol_attn.cu")]
-DEPS = [os.path.join(PKG, "csrc", f) for f in ("fused.cuh", "moments.cuh", "pool.cuh", "sm100_ptx.cuh",
-                                                "topk_router.cuh")] + [
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("sol_attn.cu", "layer_ops.cu")]
+DEPS = [os.path.join(PKG, "csrc", f) for f in ("fused.cuh", "host.h", "moments.cuh", "norm.cuh", "pool.cuh", "rope.cuh",
+                                                "rows.cuh", "sm100_ptx.cuh", "topk_router.cuh")] + [
     os.path.join(ROOT, "include", "sol_attn.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "0",
 ]
 
 

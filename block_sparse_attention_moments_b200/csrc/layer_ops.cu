@@ -1,0 +1,337 @@
+// layer_ops.cu — C ABI of the operators around the attention (declared in
+// include/sol_attn.h): argument checks and launches of the norm, rotary and
+// 8-bit product kernels.  They hold no workspace: every call reads its inputs
+// and writes its outputs only, so calls on several streams, devices or
+// captured graphs do not meet.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host.h"
+#include "norm.cuh"
+#include "rope.cuh"
+
+using namespace solattn;
+
+namespace {
+
+constexpr int kMaxC = 16384;
+constexpr int kRopeUnits = 2;   // units a thread holds: 16 warps reach H*d = 16384
+
+size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
+
+bool dtype_ok(int dtype) { return dtype == SOL_ATTN_BF16 || dtype == SOL_ATTN_FP16 || dtype == SOL_ATTN_FP32; }
+
+int sm_count(int dev, int* n) {
+  static int cached[kMaxDevices] = {0};
+  if (!cached[dev]) CUDA_TRY(cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev));
+  *n = cached[dev];
+  return SOL_ATTN_OK;
+}
+
+// The current device, checked, and its number of SMs.
+int device(int* dev, int* sms) {
+  int rc;
+  if ((rc = current_device(dev)) || (rc = check_arch(*dev))) return rc;
+  return sm_count(*dev, sms);
+}
+
+// Rows [B, L] of `width` elements of `size` bytes.
+struct Span {
+  const char* p;
+  long long sb, sl;   // bytes
+  int B, L;
+  long long width;    // bytes
+  const char* end() const { return p + (B - 1) * sb + (L - 1) * sl + width; }
+};
+
+Span span(const void* p, size_t size, long long sb, long long sl, int B, int L, long long width) {
+  const long long s = static_cast<long long>(size);
+  return Span{static_cast<const char*>(p), B > 1 ? sb * s : 0, L > 1 ? sl * s : 0, B, L, width * s};
+}
+
+// Whether two sets of rows share a byte.  Rows of equal pitch whose columns
+// lie side by side do not (two slices of one buffer); any other two whose
+// address ranges meet are taken to.
+bool overlap(const Span& a, const Span& b) {
+  if (a.end() <= b.p || b.end() <= a.p) return false;
+  if (a.sl == b.sl && a.sb == b.sb && a.L > 1) {
+    const long long d = ((b.p - a.p) % a.sl + a.sl) % a.sl;
+    if (a.sb % a.sl == 0 && d >= a.width && d + b.width <= a.sl) return false;
+  }
+  return true;
+}
+
+// Rows that are written: distinct rows may not share elements.
+bool rows_distinct(const Span& s) {
+  if (s.L > 1 && s.sl < s.width) return s.B > 1 && s.sb >= s.width && s.sl >= (s.B - 1) * s.sb + s.width;
+  return s.B <= 1 || s.sb >= (s.L - 1) * s.sl + s.width ||
+         (s.sb >= s.width && s.sl >= (s.B - 1) * s.sb + s.width);
+}
+
+bool vec16(const void* p, size_t size, std::initializer_list<long long> strides) {
+  if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  for (long long s : strides)
+    if (s * static_cast<long long>(size) % 16) return false;
+  return true;
+}
+
+int check_rows(const sol_attn_rows& r, const char* name, int B, int L) {
+  if (!dtype_ok(r.dtype)) return fail(SOL_ATTN_ERR_ARG, "%s: unknown dtype %d", name, r.dtype);
+  if (reinterpret_cast<uintptr_t>(r.data) % dtype_size(r.dtype))
+    return fail(SOL_ATTN_ERR_ALIGN, "%s is not aligned to its elements", name);
+  if ((B > 1 && r.stride_b < 0) || (L > 1 && r.stride_l < 0))
+    return fail(SOL_ATTN_ERR_ARG, "%s has a negative stride", name);
+  return SOL_ATTN_OK;
+}
+
+int convert(const sol_attn_vectors& v, const char* name, int B, int L, Vectors* out, bool* vec) {
+  *out = Vectors{};
+  if (!v.data) return SOL_ATTN_OK;
+  if (!dtype_ok(v.dtype)) return fail(SOL_ATTN_ERR_ARG, "%s: unknown dtype %d", name, v.dtype);
+  if (v.groups < 1 || L % v.groups)
+    return fail(SOL_ATTN_ERR_ARG, "%s: %d groups do not divide %d tokens", name, v.groups, L);
+  const size_t size = dtype_size(v.dtype);
+  if (reinterpret_cast<uintptr_t>(v.data) % size)
+    return fail(SOL_ATTN_ERR_ALIGN, "%s is not aligned to its elements", name);
+  out->p = v.data;
+  out->dtype = v.dtype;
+  out->sb = B > 1 ? v.stride_b : 0;
+  out->sg = v.groups > 1 ? v.stride_g : 0;
+  out->per = L / v.groups;
+  *vec = *vec && vec16(v.data, size, {out->sb, out->sg});
+  return SOL_ATTN_OK;
+}
+
+template <typename TX, typename TY, bool RES>
+int launch_norm(const NormParams& p0, bool vec, int sms, cudaStream_t st) {
+  NormParams p = p0;
+  const long long rows = static_cast<long long>(p.B) * p.L;
+  const int n = vec ? 4 : p.C <= 4096 ? 8 : 32;
+  const int per_warp = 32 * n * (vec ? 8 : 1);
+  p.warps = (p.C + per_warp - 1) / per_warp;
+  const int teams = kNormThreads / 32 / p.warps;
+  const int threads = teams * p.warps * 32;
+  const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 2LL * sms));
+  if (vec) norm_kernel<TX, TY, 8, 4, RES><<<grid, threads, 0, st>>>(p);
+  else if (n == 8) norm_kernel<TX, TY, 1, 8, RES><<<grid, threads, 0, st>>>(p);
+  else norm_kernel<TX, TY, 1, 32, RES><<<grid, threads, 0, st>>>(p);
+  CUDA_TRY(cudaGetLastError());
+  return SOL_ATTN_OK;
+}
+
+template <typename TX, typename TY>
+int launch_norm_res(const NormParams& p, bool vec, int sms, cudaStream_t st) {
+  return p.y ? launch_norm<TX, TY, true>(p, vec, sms, st) : launch_norm<TX, TY, false>(p, vec, sms, st);
+}
+
+template <typename T>
+int launch_rope(const RopeParams& p0, int sms, cudaStream_t st) {
+  RopeParams p = p0;
+  const int units = p.H * (p.d / 16);
+  p.warps = (units + 32 * kRopeUnits - 1) / (32 * kRopeUnits);
+  const size_t per_team = (p.d + (p.norm == kRopeNormHead ? 2 * units : 0)) * sizeof(float);
+  const int teams = std::max(1, std::min<int>(kRopeThreads / 32 / p.warps, static_cast<int>(40960 / per_team)));
+  const long long tokens = static_cast<long long>(p.B) * p.L;
+  const int threads = teams * p.warps * 32;
+  const int grid = static_cast<int>(std::min<long long>((tokens + teams - 1) / teams, 2LL * sms));
+  rope_kernel<T, kRopeUnits><<<grid, threads, teams * per_team, st>>>(p);
+  CUDA_TRY(cudaGetLastError());
+  return SOL_ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
+  if (!a) return fail(SOL_ATTN_ERR_ARG, "args is NULL");
+  const int B = a->B, L = a->L, C = a->C;
+  int rc;
+  if (B < 0 || L < 0 || C < 1) return fail(SOL_ATTN_ERR_ARG, "bad sizes B = %d, L = %d, C = %d", B, L, C);
+  if (C > kMaxC) return fail(SOL_ATTN_ERR_UNSUPPORTED, "C = %d exceeds the supported maximum %d", C, kMaxC);
+  if (a->norm < 0 || a->norm > 2 || a->post_norm < 0 || a->post_norm > 2)
+    return fail(SOL_ATTN_ERR_ARG, "unknown norm %d or %d", a->norm, a->post_norm);
+  if (!(a->eps >= 0.f) || !(a->post_eps >= 0.f)) return fail(SOL_ATTN_ERR_ARG, "eps must not be negative or NaN");
+  if (B == 0 || L == 0) return SOL_ATTN_OK;
+  if (static_cast<long long>(B) * L > INT_MAX) return fail(SOL_ATTN_ERR_UNSUPPORTED, "B*L exceeds 2^31 - 1");
+  if (!a->x.data) return fail(SOL_ATTN_ERR_ARG, "x is NULL");
+  if (!a->h.data && !a->q && !(a->x_out.data && a->y.data))
+    return fail(SOL_ATTN_ERR_ARG, "no output is asked for (x_out needs y)");
+  if (a->x_out.data && !a->y.data) return fail(SOL_ATTN_ERR_ARG, "x_out needs y");
+  if (a->x_inner < 1 || C % a->x_inner) return fail(SOL_ATTN_ERR_ARG, "x_inner %d does not divide C", a->x_inner);
+  if ((a->q == nullptr) != (a->q_scale == nullptr)) return fail(SOL_ATTN_ERR_ARG, "q and q_scale come together");
+
+  NormParams p{};
+  p.B = B, p.L = L, p.C = C;
+  if ((rc = check_rows(a->x, "x", B, L))) return rc;
+  const size_t xs = dtype_size(a->x.dtype);
+  int ydt = a->x.dtype;   // type of y and h
+  if (a->y.data) {
+    if ((rc = check_rows(a->y, "y", B, L))) return rc;
+    ydt = a->y.dtype;
+    if (a->h.data && a->h.dtype != ydt) return fail(SOL_ATTN_ERR_UNSUPPORTED, "h must have the type of y");
+  } else if (a->h.data) {
+    ydt = a->h.dtype;
+  }
+  if (ydt != a->x.dtype && a->x.dtype != SOL_ATTN_FP32)
+    return fail(SOL_ATTN_ERR_UNSUPPORTED, "y and h must have the type of x, or x must be fp32");
+  const size_t ys = dtype_size(ydt);
+  p.x = a->x.data;
+  p.x_sb = B > 1 ? a->x.stride_b : 0, p.x_sl = L > 1 ? a->x.stride_l : 0;
+  p.x_inner = a->x_inner, p.x_sh = a->x_inner < C ? a->x_stride_h : 0;
+  if (p.x_sh < 0) return fail(SOL_ATTN_ERR_ARG, "x has a negative stride");
+  bool vec = C % 8 == 0 && p.x_inner % 8 == 0 && vec16(p.x, xs, {p.x_sb, p.x_sl, p.x_sh});
+  const Span x = span(p.x, xs, p.x_sb, p.x_sl, B, L, (C / p.x_inner - 1) * p.x_sh + p.x_inner);
+  Span y{}, outs[3];
+  int nouts = 0;
+  if (a->y.data) {
+    p.y = a->y.data, p.y_sb = B > 1 ? a->y.stride_b : 0, p.y_sl = L > 1 ? a->y.stride_l : 0;
+    vec = vec && vec16(p.y, ys, {p.y_sb, p.y_sl});
+    y = span(p.y, ys, p.y_sb, p.y_sl, B, L, C);
+  }
+  if (a->x_out.data) {
+    if ((rc = check_rows(a->x_out, "x_out", B, L))) return rc;
+    if (a->x_out.dtype != a->x.dtype) return fail(SOL_ATTN_ERR_UNSUPPORTED, "x_out must have the type of x");
+    p.xo = a->x_out.data, p.xo_sb = B > 1 ? a->x_out.stride_b : 0, p.xo_sl = L > 1 ? a->x_out.stride_l : 0;
+    vec = vec && vec16(p.xo, xs, {p.xo_sb, p.xo_sl});
+    const Span s = span(p.xo, xs, p.xo_sb, p.xo_sl, B, L, C);
+    // in place: each row is read whole before it is written, by the same team
+    const bool in_place = p.xo == p.x && p.xo_sb == p.x_sb && p.xo_sl == p.x_sl && p.x_inner == C;
+    if (!rows_distinct(s)) return fail(SOL_ATTN_ERR_ARG, "rows of x_out share elements");
+    if ((!in_place && overlap(s, x)) || overlap(s, y))
+      return fail(SOL_ATTN_ERR_ARG, "x_out overlaps an input (only x_out = x is allowed)");
+    outs[nouts++] = s;
+  }
+  if (a->h.data) {
+    if ((rc = check_rows(a->h, "h", B, L))) return rc;
+    p.h = a->h.data, p.h_sb = B > 1 ? a->h.stride_b : 0, p.h_sl = L > 1 ? a->h.stride_l : 0;
+    vec = vec && vec16(p.h, ys, {p.h_sb, p.h_sl});
+    outs[nouts++] = span(p.h, ys, p.h_sb, p.h_sl, B, L, C);
+    if (!rows_distinct(outs[nouts - 1])) return fail(SOL_ATTN_ERR_ARG, "rows of h share elements");
+    if (overlap(outs[nouts - 1], x) || (p.y && overlap(outs[nouts - 1], y)))
+      return fail(SOL_ATTN_ERR_ARG, "h overlaps an input");
+  }
+  if (a->q) {
+    if (a->q_stride < C) return fail(SOL_ATTN_ERR_ARG, "q_stride %lld is below C", a->q_stride);
+    if (reinterpret_cast<uintptr_t>(a->q_scale) % 4) return fail(SOL_ATTN_ERR_ALIGN, "q_scale is misaligned");
+    p.q = a->q, p.q_sl = a->q_stride, p.q_scale = a->q_scale;
+    vec = vec && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.q_sl % 8 == 0;
+    outs[nouts++] = span(p.q, 1, p.q_sl * L, p.q_sl, B, L, C);
+    if (overlap(outs[nouts - 1], x) || (p.y && overlap(outs[nouts - 1], y)))
+      return fail(SOL_ATTN_ERR_ARG, "q overlaps an input");
+  }
+  for (int i = 0; i < nouts; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return fail(SOL_ATTN_ERR_ARG, "two outputs overlap");
+  if ((rc = convert(a->scale, "scale", B, L, &p.scale, &vec)) || (rc = convert(a->shift, "shift", B, L, &p.shift, &vec)) ||
+      (rc = convert(a->gate, "gate", B, L, &p.gate, &vec)) || (rc = convert(a->weight, "weight", B, L, &p.weight, &vec)) ||
+      (rc = convert(a->bias, "bias", B, L, &p.bias, &vec)) ||
+      (rc = convert(a->post_weight, "post_weight", B, L, &p.post_weight, &vec)) ||
+      (rc = convert(a->post_bias, "post_bias", B, L, &p.post_bias, &vec)))
+    return rc;
+  p.rs = a->residual_scale;
+  p.pre = a->norm, p.post = a->post_norm;
+  p.pre_eps = a->eps, p.post_eps = a->post_eps;
+
+  int dev, sms;
+  if ((rc = device(&dev, &sms))) return rc;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, sms, st);
+  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, sms, st);
+  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, sms, st);
+  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, sms, st);
+  return launch_norm_res<float, float>(p, vec, sms, st);
+}
+
+int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
+  if (!a) return fail(SOL_ATTN_ERR_ARG, "args is NULL");
+  const int B = a->B, L = a->L, H = a->H, d = a->d;
+  int rc;
+  if (B < 0 || L < 0 || H < 1 || d < 1) return fail(SOL_ATTN_ERR_ARG, "bad sizes B = %d, L = %d, H = %d, d = %d", B, L, H, d);
+  if (d % 16 || d > kRopeMaxD) return fail(SOL_ATTN_ERR_UNSUPPORTED, "d must be a multiple of 16 up to 256 (got %d)", d);
+  if (static_cast<long long>(H) * d > kMaxC)
+    return fail(SOL_ATTN_ERR_UNSUPPORTED, "H*d = %lld exceeds the supported maximum %d", static_cast<long long>(H) * d, kMaxC);
+  if (!dtype_ok(a->dtype)) return fail(SOL_ATTN_ERR_ARG, "unknown dtype %d", a->dtype);
+  if (a->norm < 0 || a->norm > 2) return fail(SOL_ATTN_ERR_ARG, "unknown norm %d", a->norm);
+  if (!(a->eps >= 0.f)) return fail(SOL_ATTN_ERR_ARG, "eps must not be negative or NaN");
+  if (a->pairing != SOL_ATTN_PAIR_INTERLEAVED && a->pairing != SOL_ATTN_PAIR_HALF)
+    return fail(SOL_ATTN_ERR_ARG, "unknown pairing %d", a->pairing);
+  if (!a->freqs || !a->axis) return fail(SOL_ATTN_ERR_ARG, "freqs or axis is NULL");
+  if (a->axes < 1 || a->axes > kRopeMaxAxes) return fail(SOL_ATTN_ERR_UNSUPPORTED, "%d axes (1 to %d)", a->axes, kRopeMaxAxes);
+  RopeParams p{};
+  for (int i = 0; i < d / 2; ++i) {
+    if (!std::isfinite(a->freqs[i])) return fail(SOL_ATTN_ERR_ARG, "frequency %d is not finite", i);
+    if (a->axis[i] >= a->axes) return fail(SOL_ATTN_ERR_ARG, "pair %d is on axis %d of %d", i, a->axis[i], a->axes);
+    p.turns[i] = a->freqs[i] / 6.283185307179586476925286766559;
+    p.axis[i] = a->axis[i];
+  }
+  if (a->pos_kind == SOL_ATTN_POS_GRID) {
+    const long long f = a->grid_f, h = a->grid_h, w = a->grid_w;
+    if (a->axes != 3) return fail(SOL_ATTN_ERR_ARG, "a grid has 3 axes");
+    if (f < 1 || h < 1 || w < 1 || f > INT_MAX / h || f * h > INT_MAX / w)
+      return fail(SOL_ATTN_ERR_ARG, "bad grid %lld x %lld x %lld", f, h, w);
+    if (a->start < 0) return fail(SOL_ATTN_ERR_ARG, "start is negative");
+    p.grid_h = a->grid_h, p.grid_w = a->grid_w, p.grid_tokens = f * h * w, p.start = a->start;
+  } else {
+    if (a->pos_kind < SOL_ATTN_POS_GRID || a->pos_kind > SOL_ATTN_POS_F64)
+      return fail(SOL_ATTN_ERR_ARG, "unknown kind of positions %d", a->pos_kind);
+    p.pos = a->positions;
+    p.pos_sb = a->pos_stride_b, p.pos_sl = a->pos_stride_l, p.pos_sa = a->pos_stride_a;
+  }
+  p.pos_kind = a->pos_kind;
+  if (B == 0 || L == 0) return SOL_ATTN_OK;
+  if (static_cast<long long>(B) * L > INT_MAX) return fail(SOL_ATTN_ERR_UNSUPPORTED, "B*L exceeds 2^31 - 1");
+  if (p.pos_kind != kPosGrid) {
+    const size_t s = p.pos_kind == kPosI32 || p.pos_kind == kPosF32 ? 4 : 8;
+    if (!p.pos) return fail(SOL_ATTN_ERR_ARG, "positions is NULL");
+    if (reinterpret_cast<uintptr_t>(p.pos) % s) return fail(SOL_ATTN_ERR_ALIGN, "positions is not aligned to its elements");
+  }
+  p.B = B, p.L = L, p.H = H, p.d = d;
+  p.norm = a->norm, p.eps = a->eps;
+  p.half = a->pairing == SOL_ATTN_PAIR_HALF;
+  const size_t size = dtype_size(a->dtype);
+  const long long n = static_cast<long long>(B) * H * L * d;
+  const sol_attn_rope_tensor* in[3] = {&a->q, &a->k, &a->v};
+  RopeTensor* out[3] = {&p.q, &p.k, &p.v};
+  const char* names[3] = {"q", "k", "v"};
+  for (int i = 0; i < 3; ++i) {
+    const sol_attn_rope_tensor& t = *in[i];
+    if (i == 2 && !t.in && !t.out) continue;
+    if ((rc = check_ptr(t.in, names[i])) || (rc = check_ptr(t.out, names[i]))) return rc;
+    RopeTensor& r = *out[i];
+    r.in = t.in, r.out = t.out;
+    r.sb = B > 1 ? t.stride_b : 0, r.sl = L > 1 ? t.stride_l : 0, r.sh = H > 1 ? t.stride_h : 0;
+    if (r.sb < 0 || r.sl < 0 || r.sh < 0) return fail(SOL_ATTN_ERR_ARG, "%s has a negative stride", names[i]);
+    if (!vec16(t.in, size, {r.sb, r.sl, r.sh}))
+      return fail(SOL_ATTN_ERR_ALIGN, "%s: strides must be multiples of 16 bytes", names[i]);
+    if (i < 2 && t.weight) {
+      if (a->norm == kRopeNormNone) return fail(SOL_ATTN_ERR_ARG, "%s has a weight but no norm", names[i]);
+      if (!dtype_ok(t.weight_dtype)) return fail(SOL_ATTN_ERR_ARG, "%s weight: unknown dtype %d", names[i], t.weight_dtype);
+      if (reinterpret_cast<uintptr_t>(t.weight) % 16) return fail(SOL_ATTN_ERR_ALIGN, "%s weight is not 16-byte aligned", names[i]);
+      r.weight = t.weight, r.weight_dtype = t.weight_dtype;
+    }
+  }
+  const int tensors = p.v.in ? 3 : 2;
+  for (int i = 0; i < tensors; ++i) {
+    const char* o = static_cast<const char*>(out[i]->out);
+    const char* o_end = o + n * static_cast<long long>(size);
+    for (int j = 0; j < tensors; ++j) {
+      const RopeTensor& t = *out[j];
+      const char* x = static_cast<const char*>(t.in);
+      const char* x_end = x + ((B - 1) * t.sb + (L - 1) * t.sl + (H - 1) * t.sh + d) * static_cast<long long>(size);
+      if (o < x_end && x < o_end) return fail(SOL_ATTN_ERR_ARG, "an output overlaps an input tensor");
+      const char* o2 = static_cast<const char*>(t.out);
+      if (j != i && o < o2 + n * static_cast<long long>(size) && o2 < o_end)
+        return fail(SOL_ATTN_ERR_ARG, "two outputs overlap");
+    }
+  }
+  int dev, sms;
+  if ((rc = device(&dev, &sms))) return rc;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (a->dtype == SOL_ATTN_BF16) return launch_rope<__nv_bfloat16>(p, sms, st);
+  if (a->dtype == SOL_ATTN_FP16) return launch_rope<__half>(p, sms, st);
+  return launch_rope<float>(p, sms, st);
+}
+
+}  // extern "C"

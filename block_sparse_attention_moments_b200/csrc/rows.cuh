@@ -1,0 +1,208 @@
+// rows.cuh — what the row-wise kernels (norm.cuh, rope.cuh) share: loads and
+// stores of V elements with their conversion to fp32, and reductions over a
+// team, a group of whole warps that works on one row together.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace solattn {
+
+enum : int { kDtypeBf16 = 0, kDtypeFp16 = 1, kDtypeFp32 = 2 };
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f32(float x) { return x; }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ float from_f32(float x) { return x; }
+
+// V elements as they lie in memory: V = 8 moves 16-byte vectors (two of them
+// for fp32), V = 1 single elements, for rows whose address or width is odd.
+template <typename T, int V>
+struct Raw;
+template <typename T>
+struct Raw<T, 8> {
+  static constexpr int kVecs = sizeof(T) / 2;   // 16-byte vectors
+  uint4 r[kVecs];
+};
+template <typename T>
+struct Raw<T, 1> {
+  T r;
+};
+
+// Streaming load: each input element is read once, so it does not displace
+// the modulation vectors in L1.  Not the non-coherent path: a row may be
+// written in place by the thread that read it.
+__device__ __forceinline__ uint4 ld_row_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw<T, 8>& v, const T* p) {
+#pragma unroll
+  for (int i = 0; i < Raw<T, 8>::kVecs; ++i) v.r[i] = ld_row_v4(reinterpret_cast<const uint4*>(p) + i);
+}
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw<T, 1>& v, const T* p) {
+  v.r = *p;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen2(uint32_t w, float& a, float& b);
+template <>
+__device__ __forceinline__ void widen2<__nv_bfloat16>(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xFFFF0000u);
+}
+template <>
+__device__ __forceinline__ void widen2<__half>(uint32_t w, float& a, float& b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const Raw<T, 8>& v, float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(v.r[i].x);
+      f[4 * i + 1] = __uint_as_float(v.r[i].y);
+      f[4 * i + 2] = __uint_as_float(v.r[i].z);
+      f[4 * i + 3] = __uint_as_float(v.r[i].w);
+    }
+  } else {
+    widen2<T>(v.r[0].x, f[0], f[1]);
+    widen2<T>(v.r[0].y, f[2], f[3]);
+    widen2<T>(v.r[0].z, f[4], f[5]);
+    widen2<T>(v.r[0].w, f[6], f[7]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Raw<T, 1>& v, float (&f)[1]) {
+  f[0] = to_f32<T>(v.r);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&f)[8]) {
+  uint4* q = reinterpret_cast<uint4*>(p);
+  if constexpr (sizeof(T) == 4) {
+    q[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    q[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  } else {
+    q[0] = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]), narrow2<T>(f[6], f[7]));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&f)[1]) {
+  *p = from_f32<T>(f[0]);
+}
+
+// V consecutive elements of a vector of parameters whose type is only known at run time.
+template <int V>
+__device__ __forceinline__ void load_param(const void* p, int dtype, long long at, float (&f)[V]) {
+  if constexpr (V == 8) {
+    if (dtype == kDtypeFp32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      const float4 a = q[0], b = q[1];
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (dtype == kDtypeBf16) widen2<__nv_bfloat16>(w[i], f[2 * i], f[2 * i + 1]);
+        else widen2<__half>(w[i], f[2 * i], f[2 * i + 1]);
+      }
+    }
+  } else {
+    f[0] = dtype == kDtypeFp32   ? static_cast<const float*>(p)[at]
+           : dtype == kDtypeBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at])
+                                 : __half2float(static_cast<const __half*>(p)[at]);
+  }
+}
+
+// ------------------------------------------------------------------ teams
+// A team is `warps` whole warps of a block, numbered from 0; a block holds up
+// to 15 teams of more than one warp (each has a named barrier of its own,
+// barrier 0 being the block's).  Every warp of a team takes the same calls.
+struct Team {
+  int warps;      // warps of a team
+  int index;      // this team's number in the block
+  int warp;       // this warp's number in the team
+  float* slots;   // shared memory, 2 * warps floats of this team
+  int turn;       // which half of the slots the next reduction writes
+};
+
+__device__ __forceinline__ void team_sync(const Team& t) {
+  if (t.warps == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(t.index + 1), "r"(t.warps * 32) : "memory");
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// Sum over the team, the same bits in every thread and on every run: lanes by
+// a butterfly, warps in their order.  The two halves of the slots alternate,
+// so that one barrier is enough: a warp that is one reduction ahead writes the
+// other half, and it cannot be two ahead.
+__device__ __forceinline__ float team_sum(Team& t, float x) {
+  x = warp_sum(x);
+  if (t.warps == 1) return x;
+  float* s = t.slots + t.turn * t.warps;
+  t.turn ^= 1;
+  if ((threadIdx.x & 31) == 0) s[t.warp] = x;
+  team_sync(t);
+  float r = 0.f;
+  for (int i = 0; i < t.warps; ++i) r += s[i];
+  return r;
+}
+
+// Maximum of bit patterns.  Of absolute values it is the largest one, and a
+// NaN's pattern is above that of infinity, so a NaN anywhere comes through.
+__device__ __forceinline__ uint32_t team_max(Team& t, uint32_t x) {
+  x = __reduce_max_sync(0xFFFFFFFFu, x);
+  if (t.warps == 1) return x;
+  float* s = t.slots + t.turn * t.warps;
+  t.turn ^= 1;
+  if ((threadIdx.x & 31) == 0) s[t.warp] = __uint_as_float(x);
+  team_sync(t);
+  uint32_t r = 0;
+  for (int i = 0; i < t.warps; ++i) r = max(r, __float_as_uint(s[i]));
+  return r;
+}
+
+}  // namespace solattn

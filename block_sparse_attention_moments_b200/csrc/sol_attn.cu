@@ -6,13 +6,12 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <string>
 
 #include "fused.cuh"
+#include "host.h"
 #include "moments.cuh"
 #include "pool.cuh"
 #include "sol_attn.h"
@@ -27,24 +26,6 @@ constexpr int kMaxL = 1 << 20;
 constexpr int kMaxBH = 65535;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;  // bounded device waits: 2 s
 constexpr unsigned long long kTestTimeoutNs = 1000000ull;  // with SOL_ATTN_FLAG_TEST_STALL: 1 ms
-
-thread_local std::string g_last_error;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-#define CUDA_TRY(expr)                                                                        \
-  do {                                                                                        \
-    cudaError_t e_ = (expr);                                                                  \
-    if (e_ != cudaSuccess) return fail(SOL_ATTN_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_)); \
-  } while (0)
 
 // ------------------------------------------------------------------ workspace
 struct Shape {
@@ -83,7 +64,6 @@ struct Workspace {
   cudaEvent_t ev_in[2] = {nullptr, nullptr}, ev_comp[2] = {nullptr, nullptr}, ev_out[2] = {nullptr, nullptr};
 };
 
-constexpr int kMaxDevices = 64;
 Workspace g_ws[kMaxDevices];
 std::mutex g_mu;
 
@@ -119,25 +99,6 @@ size_t layout(const Shape& s, Workspace* w, char* base) {
     w->counts = reinterpret_cast<int*>(p_cnt);
   }
   return off;
-}
-
-int current_device(int* dev) {
-  CUDA_TRY(cudaGetDevice(dev));
-  if (*dev < 0 || *dev >= kMaxDevices) return fail(SOL_ATTN_ERR_UNSUPPORTED, "device index %d too large", *dev);
-  return SOL_ATTN_OK;
-}
-
-int check_arch(int dev) {
-  static int checked[kMaxDevices] = {0};
-  if (checked[dev] == 1) return SOL_ATTN_OK;
-  int major = 0, minor = 0;
-  CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-  CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-  if (major != 10 || minor != 0)
-    return fail(SOL_ATTN_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a", dev, major,
-                minor);
-  checked[dev] = 1;
-  return SOL_ATTN_OK;
 }
 
 // Make the workspace of the current device fit shape s (grow-only allocation).
@@ -183,32 +144,7 @@ int check_shape(int B, int H, int L, int d, int block) {
   return SOL_ATTN_OK;
 }
 
-int check_ptr(const void* p, const char* name) {
-  if (!p) return fail(SOL_ATTN_ERR_ARG, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(SOL_ATTN_ERR_ALIGN, "%s is not 16-byte aligned", name);
-  return SOL_ATTN_OK;
-}
-
 // ------------------------------------------------------------------ TMA descriptors
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-int get_encoder(EncodeTiledFn* fn) {
-  static EncodeTiledFn cached = nullptr;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    err = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
-    if (err == cudaSuccess && q == cudaDriverEntryPointSuccess) cached = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  if (!cached) return fail(SOL_ATTN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(err));
-  *fn = cached;
-  return SOL_ATTN_OK;
-}
-
 // 3-D bf16 map over [BH][rows][d] with a {64, box_rows, 1} box and 128-byte swizzle.
 // Rows past `rows` read as zero.
 int make_map(CUtensorMap* m, const void* ptr, int d, long long rows, long long BH, int box_rows) {

@@ -199,6 +199,124 @@ int sol_attn_topk_route(int B, int H, int L, int d, int block, int k, uint32_t* 
  * run on this device.  Pass the stream the forward was enqueued on. */
 int sol_attn_noalloc_status(void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the attention of a diffusion-transformer layer (the paper
+ * has no counterpart; it runs inside such layers): norms with modulation, gate
+ * and residual, rotary positions with several axes, and products of 8-bit
+ * integers.
+ *
+ * They keep no workspace and no state: a call enqueues one kernel on stream,
+ * may be captured into a graph from its first call on, and may run beside any
+ * other call.  The current device must be the tensors' own.  Strides are in
+ * elements and not negative; the channels of a token are contiguous.  B = 0 or
+ * L = 0 returns SOL_ATTN_OK and enqueues nothing.  Sums and statistics are
+ * fp32 (products of 8-bit integers: exact in 32-bit integers), and every
+ * output is rounded once.  Two runs on the same inputs give the same bits. */
+
+/* Element types. */
+#define SOL_ATTN_BF16 0
+#define SOL_ATTN_FP16 1
+#define SOL_ATTN_FP32 2
+
+/* Norms of sol_attn_norm_args. */
+#define SOL_ATTN_NORM_NONE 0
+#define SOL_ATTN_NORM_LAYER 1
+#define SOL_ATTN_NORM_RMS 2
+
+/* Tokens [B, L, C]: element (b, l, c) at data[b*stride_b + l*stride_l + c]. */
+typedef struct sol_attn_rows {
+  void* data;
+  int dtype;
+  long long stride_b, stride_l;
+} sol_attn_rows;
+
+/* Vectors [B, groups, C] of modulation, each for L / groups consecutive tokens
+ * (groups must divide L); a vector of weights is groups = 1, stride_b = 0.
+ * data NULL: absent. */
+typedef struct sol_attn_vectors {
+  const void* data;
+  int dtype;
+  int groups;
+  long long stride_b, stride_g;
+} sol_attn_vectors;
+
+/* Arguments of sol_attn_norm_modulate.  Zero means absent for every pointer. */
+typedef struct sol_attn_norm_args {
+  int B, L, C;                   /* 1 <= C <= 16384 */
+  int x_inner;                   /* x holds C / x_inner pieces of x_inner channels, */
+  long long x_stride_h;          /* x_stride_h apart; x_inner = C: contiguous rows  */
+  sol_attn_rows x;               /* bf16, fp16 or fp32 */
+  sol_attn_rows y;               /* output of the block before; its type and h's are the
+                                    same: x's own, or any where x is fp32 */
+  sol_attn_rows x_out;           /* x', type of x; may be x itself (in place); needs y */
+  sol_attn_rows h;
+  int8_t* q;                     /* h in 8 bits, row b*L + l at q + (b*L + l)*q_stride */
+  long long q_stride;
+  float* q_scale;                /* [B*L] */
+  float residual_scale;
+  int norm;                      /* SOL_ATTN_NORM_* before the modulation */
+  float eps;
+  int post_norm;                 /* SOL_ATTN_NORM_* of y */
+  float post_eps;
+  sol_attn_vectors scale, shift, gate;
+  sol_attn_vectors weight, bias, post_weight, post_bias;
+} sol_attn_norm_args;
+
+/* One pass over the rows of a residual stream:
+ *   x' = residual_scale * x + gate * post_norm(y)     (without y: x' = x)
+ *   h  = norm(x') * (1 + scale) + shift
+ * with norm(v) = (v - mean) / sqrt(var + eps) * weight + bias (layer),
+ * v / sqrt(mean(v^2) + eps) * weight + bias (rms) or v * weight + bias (none).
+ * Outputs, each where wanted: x', h, and h in 8 bits: q_scale = max|h| / 127 of
+ * the row and q = h / q_scale to the nearest whole number, ties to even.  A row
+ * of zeros has the scale 0; a row that holds an infinity or a NaN has a scale
+ * that is not finite and zeros for q. */
+int sol_attn_norm_modulate(const sol_attn_norm_args* args, void* stream);
+
+/* Norms of q and k (SOL_ATTN_ROPE_NORM_*), pairings and positions of sol_attn_rope. */
+#define SOL_ATTN_ROPE_NORM_NONE 0
+#define SOL_ATTN_ROPE_NORM_HEAD 1   /* RMS over the d channels of each head, weight [d] */
+#define SOL_ATTN_ROPE_NORM_TOKEN 2  /* RMS over the H*d channels of a token, weight [H*d] */
+#define SOL_ATTN_PAIR_INTERLEAVED 0 /* pair i is channels 2i and 2i + 1 of a head */
+#define SOL_ATTN_PAIR_HALF 1        /* pair i is channels i and i + d/2 */
+#define SOL_ATTN_POS_GRID 0         /* (frame, row, column) of raster index start + l */
+#define SOL_ATTN_POS_I32 1          /* positions [B, L, axes] of this type */
+#define SOL_ATTN_POS_I64 2
+#define SOL_ATTN_POS_F32 3
+#define SOL_ATTN_POS_F64 4
+
+typedef struct sol_attn_rope_tensor {
+  const void* in;                /* [B, L, H, d], any strides that are multiples of 16 bytes */
+  long long stride_b, stride_l, stride_h;
+  void* out;                     /* contiguous [B, H, L, d]; overlaps no input */
+  const void* weight;            /* of the norm; NULL: ones */
+  int weight_dtype;
+} sol_attn_rope_tensor;
+
+typedef struct sol_attn_rope_args {
+  int B, L, H, d;                /* d a multiple of 16 up to 256, H*d <= 16384 */
+  int dtype;                     /* of q, k and v */
+  sol_attn_rope_tensor q, k, v;  /* v.in and v.out NULL: no v */
+  int norm;
+  float eps;
+  int pairing;
+  int axes;                      /* 1 to 4 */
+  const double* freqs;           /* host, [d/2]: angle of pair i per unit of position */
+  const unsigned char* axis;     /* host, [d/2]: axis of pair i */
+  int pos_kind;
+  int grid_f, grid_h, grid_w;    /* SOL_ATTN_POS_GRID (3 axes) */
+  long long start;               /* raster index of token 0; tokens at or past the grid's
+                                    end keep the position 0 */
+  const void* positions;         /* else: device, [B, L, axes], any strides */
+  long long pos_stride_b, pos_stride_l, pos_stride_a;
+} sol_attn_rope_args;
+
+/* Makes q, k and v of one projection ready for the attention: RMS norm of q
+ * and k, rotation of their pairs (a, b) -> (a cos t - b sin t, a sin t + b cos t)
+ * by t = position[axis] * freq, and the layout [B, H, L, d].  v is copied.
+ * Angles are formed in fp64. */
+int sol_attn_rope(const sol_attn_rope_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
