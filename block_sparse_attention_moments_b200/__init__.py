@@ -21,7 +21,7 @@ __all__ = [
     "forward", "stats", "forward_host", "stage_pool", "stage_threshold", "stage_fused",
     "workspace_bytes", "release", "kernels_per_forward", "DebugBuffers", "EXPORTED_SYMBOLS", "topk_route",
     "executed_flops", "BLOCK", "norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope",
-    "rope_axes",
+    "rope_axes", "int8_linear", "linear_status",
 ]
 
 FLAG_SELECT_ALL = 0x1
@@ -44,6 +44,7 @@ EXPORTED_SYMBOLS = (
     "sol_attn_workspace_bytes", "sol_attn_release", "sol_attn_error_string",
     "sol_attn_kernels_per_forward", "sol_attn_forward_noalloc", "sol_attn_profile_read",
     "sol_attn_noalloc_status", "sol_attn_topk_route", "sol_attn_norm_modulate", "sol_attn_rope",
+    "sol_attn_quantized_linear", "sol_attn_linear_status",
 )
 
 
@@ -92,10 +93,13 @@ def lib():
     L.sol_attn_topk_route.argtypes = [i, i, i, i, i, i, vp, vp]
     L.sol_attn_norm_modulate.argtypes = [vp, vp]
     L.sol_attn_rope.argtypes = [vp, vp]
+    L.sol_attn_quantized_linear.argtypes = [vp, vp]
+    L.sol_attn_linear_status.argtypes = [vp]
     for name in ("sol_attn_forward", "sol_attn_forward_ex", "sol_attn_stats", "sol_attn_forward_host",
                  "sol_attn_stage_pool", "sol_attn_stage_threshold", "sol_attn_stage_fused", "sol_attn_release",
                  "sol_attn_kernels_per_forward", "sol_attn_forward_noalloc", "sol_attn_profile_read",
-                 "sol_attn_noalloc_status", "sol_attn_topk_route", "sol_attn_norm_modulate", "sol_attn_rope"):
+                 "sol_attn_noalloc_status", "sol_attn_topk_route", "sol_attn_norm_modulate", "sol_attn_rope",
+                 "sol_attn_quantized_linear", "sol_attn_linear_status"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -285,7 +289,8 @@ def executed_flops(selected_pairs: int, B: int, H: int, L: int, d: int, *, appro
 
 
 # The operators around the attention import torch, which this module does only where it is used.
-_LAYER_OPS = ("norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes")
+_LAYER_OPS = ("norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes",
+              "int8_linear", "linear_status")
 
 
 def __getattr__(name):

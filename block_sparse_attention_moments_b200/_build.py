@@ -10,8 +10,9 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libsol_attn.so")
 PROFILE_LIB = os.path.join(PKG, "libsol_attn_profile.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("sol_attn.cu", "layer_ops.cu")]
-DEPS = [os.path.join(PKG, "csrc", f) for f in ("fused.cuh", "host.h", "moments.cuh", "norm.cuh", "pool.cuh", "rope.cuh",
-                                                "rows.cuh", "sm100_ptx.cuh", "topk_router.cuh")] + [
+DEPS = [os.path.join(PKG, "csrc", f) for f in ("fused.cuh", "host.h", "linear.cuh", "moments.cuh", "norm.cuh",
+                                                "pool.cuh", "rope.cuh", "rows.cuh", "sm100_ptx.cuh",
+                                                "topk_router.cuh")] + [
     os.path.join(ROOT, "include", "sol_attn.h")]
 
 NVCC_FLAGS = [

@@ -6,8 +6,10 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "host.h"
+#include "linear.cuh"
 #include "norm.cuh"
 #include "rope.cuh"
 
@@ -16,6 +18,7 @@ using namespace solattn;
 namespace {
 
 constexpr int kMaxC = 16384;
+constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
 constexpr int kRopeUnits = 2;   // units a thread holds: 16 warps reach H*d = 16384
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
@@ -138,6 +141,80 @@ int launch_rope(const RopeParams& p0, int sms, cudaStream_t st) {
   rope_kernel<T, kRopeUnits><<<grid, threads, teams * per_team, st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
+}
+
+// 2-D map of rows of K elements (pitch in bytes) with a {box_k, box_rows} box
+// and 128-byte swizzle; what lies outside reads as zero and is not written.
+int make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long K, long long rows,
+                long long pitch, int box_k, int box_rows) {
+  EncodeTiledFn enc;
+  int rc = get_encoder(&enc);
+  if (rc) return rc;
+  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  cuuint64_t gstride[1] = {static_cast<cuuint64_t>(pitch)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, type, 2, const_cast<void*>(ptr), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SOL_ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return SOL_ATTN_OK;
+}
+
+template <typename T>
+constexpr CUtensorMapDataType map_type() {
+  return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+struct LinearOperands {
+  const int8_t* a;
+  long long a_pitch;
+  const int8_t* w;
+  long long w_pitch;
+};
+
+template <int CG, int BN, typename T>
+int launch_linear(const LinearParams& p0, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
+  using C = LinearConfig<CG, BN>;
+  LinearParams p = p0;
+  p.tiles_m = (p.M + 128 * CG - 1) / (128 * CG);
+  p.tiles_n = (p.N + BN - 1) / BN;
+  p.band = 8;
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  if (tiles > INT_MAX / 2) return fail(SOL_ATTN_ERR_UNSUPPORTED, "%lld output tiles", tiles);
+  CUtensorMap ma, mw, mo{};
+  int rc;
+  if ((rc = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.a, p.K, p.M, o.a_pitch, 128, 128))) return rc;
+  if ((rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.w, p.K, p.N, o.w_pitch, 128, BN / CG))) return rc;
+  p.direct = reinterpret_cast<uintptr_t>(p.out) % 16 != 0 || p.out_pitch * sizeof(T) % 16 != 0;
+  if (!p.direct &&
+      (rc = make_map_2d(&mo, map_type<T>(), p.out, p.N, p.M, p.out_pitch * sizeof(T), 128 / sizeof(T), 32)))
+    return rc;
+  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
+  if (!attr_set[dev]) {
+    CUDA_TRY(cudaFuncSetAttribute(linear_kernel<CG, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(C::kSmem)));
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(CG * static_cast<unsigned>(std::min<long long>(tiles, sms / CG)));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_kernel<CG, BN, T>, ma, mw, mo, p));
+  return SOL_ATTN_OK;
+}
+
+template <typename T>
+int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
+  if (p.M > 128) return launch_linear<2, 256, T>(p, o, dev, sms, st);
+  return launch_linear<1, 128, T>(p, o, dev, sms, st);
 }
 
 }  // namespace
@@ -332,6 +409,65 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
   if (a->dtype == SOL_ATTN_BF16) return launch_rope<__nv_bfloat16>(p, sms, st);
   if (a->dtype == SOL_ATTN_FP16) return launch_rope<__half>(p, sms, st);
   return launch_rope<float>(p, sms, st);
+}
+
+int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
+  if (!a) return fail(SOL_ATTN_ERR_ARG, "args is NULL");
+  const int M = a->M, N = a->N, K = a->K;
+  int rc;
+  if (M < 0 || N < 0 || K < 1) return fail(SOL_ATTN_ERR_ARG, "bad sizes M = %d, N = %d, K = %d", M, N, K);
+  if (K > kMaxLinearK) return fail(SOL_ATTN_ERR_UNSUPPORTED, "K = %d exceeds %d, up to which the sums fit 32 bits", K, kMaxLinearK);
+  if (!dtype_ok(a->out_dtype)) return fail(SOL_ATTN_ERR_ARG, "out: unknown dtype %d", a->out_dtype);
+  if (M == 0 || N == 0) return SOL_ATTN_OK;
+  if ((rc = check_ptr(a->a, "a")) || (rc = check_ptr(a->w, "w"))) return rc;
+  if (!a->a_scale || !a->w_scale || !a->out) return fail(SOL_ATTN_ERR_ARG, "a_scale, w_scale or out is NULL");
+  if ((M > 1 && a->a_stride < K) || (N > 1 && a->w_stride < K))
+    return fail(SOL_ATTN_ERR_ARG, "a row pitch is below K");
+  if ((M > 1 && a->a_stride % 16) || (N > 1 && a->w_stride % 16))
+    return fail(SOL_ATTN_ERR_ALIGN, "the rows of a and w must start at multiples of 16 bytes");
+  if (M > 1 && a->out_stride < N) return fail(SOL_ATTN_ERR_ARG, "out_stride is below N");
+  const size_t size = dtype_size(a->out_dtype);
+  if (reinterpret_cast<uintptr_t>(a->a_scale) % 4 || reinterpret_cast<uintptr_t>(a->w_scale) % 4 ||
+      reinterpret_cast<uintptr_t>(a->out) % size)
+    return fail(SOL_ATTN_ERR_ALIGN, "a_scale, w_scale or out is not aligned to its elements");
+  LinearParams p{};
+  p.M = M, p.N = N, p.K = K;
+  p.a_scale = a->a_scale, p.w_scale = a->w_scale;
+  if (a->bias) {
+    if (!dtype_ok(a->bias_dtype)) return fail(SOL_ATTN_ERR_ARG, "bias: unknown dtype %d", a->bias_dtype);
+    if (reinterpret_cast<uintptr_t>(a->bias) % dtype_size(a->bias_dtype))
+      return fail(SOL_ATTN_ERR_ALIGN, "bias is not aligned to its elements");
+    p.bias = a->bias, p.bias_dtype = a->bias_dtype;
+  }
+  // a pitch that no row uses may be anything: the maps take one that fits
+  const long long fit = (K + 15LL) / 16 * 16;
+  LinearOperands o{a->a, M > 1 ? a->a_stride : fit, a->w, N > 1 ? a->w_stride : fit};
+  p.out = a->out;
+  p.out_pitch = M > 1 ? a->out_stride : (N + 7LL) / 8 * 8;
+  const Span out = span(p.out, size, 0, p.out_pitch, 1, M, N);
+  if (overlap(out, span(o.a, 1, 0, o.a_pitch, 1, M, K)) || overlap(out, span(o.w, 1, 0, o.w_pitch, 1, N, K)) ||
+      overlap(out, span(p.a_scale, 4, 0, 0, 1, 1, M)) || overlap(out, span(p.w_scale, 4, 0, 0, 1, 1, N)) ||
+      (p.bias && overlap(out, span(p.bias, dtype_size(p.bias_dtype), 0, 0, 1, 1, N))))
+    return fail(SOL_ATTN_ERR_ARG, "out overlaps an input");
+  int dev, sms;
+  if ((rc = device(&dev, &sms))) return rc;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (a->out_dtype == SOL_ATTN_BF16) return run_linear<__nv_bfloat16>(p, o, dev, sms, st);
+  if (a->out_dtype == SOL_ATTN_FP16) return run_linear<__half>(p, o, dev, sms, st);
+  return run_linear<float>(p, o, dev, sms, st);
+}
+
+int sol_attn_linear_status(void* stream) {
+  int dev, sms, rc;
+  if ((rc = device(&dev, &sms))) return rc;
+  auto st = static_cast<cudaStream_t>(stream);
+  CUDA_TRY(cudaStreamSynchronize(st));
+  unsigned h = 0;
+  CUDA_TRY(cudaMemcpyFromSymbol(&h, g_linear_status, sizeof(h)));
+  if (!h) return SOL_ATTN_OK;
+  const unsigned zero = 0;
+  CUDA_TRY(cudaMemcpyToSymbol(g_linear_status, &zero, sizeof(zero)));
+  return fail(SOL_ATTN_ERR_TIMEOUT, "a bounded device wait of a product gave up (status 0x%x)", h);
 }
 
 }  // extern "C"

@@ -1,7 +1,7 @@
 """Operators around the attention of a diffusion-transformer layer.
 
-Thin bindings of sol_attn_norm_modulate and sol_attn_rope in
-``include/sol_attn.h``: they check tensor properties, allocate the outputs and
+Thin bindings of sol_attn_norm_modulate, sol_attn_rope and
+sol_attn_quantized_linear in ``include/sol_attn.h``: they check tensor properties, allocate the outputs and
 marshal pointers; all arithmetic runs in the library's CUDA kernels.  Forward
 only, as the attention is: a call whose inputs ask for gradients is refused.
 
@@ -19,7 +19,8 @@ import torch
 
 from . import _check, lib
 
-__all__ = ["norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes"]
+__all__ = ["norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes",
+           "int8_linear", "linear_status"]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -56,6 +57,12 @@ class _RopeArgs(ctypes.Structure):
                 ("v", _RopeTensor), ("norm", _i), ("eps", _f), ("pairing", _i), ("axes", _i), ("freqs", _vp),
                 ("axis", _vp), ("pos_kind", _i), ("grid_f", _i), ("grid_h", _i), ("grid_w", _i), ("start", _ll),
                 ("positions", _vp), ("pos_stride_b", _ll), ("pos_stride_l", _ll), ("pos_stride_a", _ll)]
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = [("M", _i), ("N", _i), ("K", _i), ("a", _vp), ("a_stride", _ll), ("a_scale", _vp), ("w", _vp),
+                ("w_stride", _ll), ("w_scale", _vp), ("bias", _vp), ("bias_dtype", _i), ("out", _vp), ("out_dtype", _i),
+                ("out_stride", _ll)]
 
 
 # ------------------------------------------------------------------ checks
@@ -377,3 +384,59 @@ def rope(q, k, v=None, *, grid=None, positions=None, axes=None, start=0, theta=1
     if B and L and H:
         _check(lib().sol_attn_rope(ctypes.byref(a), _stream(dev)))
     return tuple(outs)
+
+
+# ------------------------------------------------------------------ products of 8-bit integers
+def _scales(t, name, n, device):
+    _input(t, name, device, (torch.float32,))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous values (got {list(t.shape)})")
+
+
+@_placed
+def int8_linear(a, a_scale, w, w_scale, bias=None, *, out_dtype=None, out=None):
+    """(a @ w.T) * a_scale[:, None] * w_scale + bias for 8-bit a and w, summed exactly.
+
+    a: int8 [M, K] or [B, L, K] with fp32 scales [M] or [B, L], such as (q, s) of quantize_rows or
+    norm_modulate(quantize=True); w: int8 [N, K] with fp32 scales [N], such as quantize_rows of a weight matrix.  The
+    rows of both start at multiples of 16 bytes (as those calls return them); K is at most 131071.  bias: [N], bf16,
+    fp16 or fp32.  Returns [M, N] or [B, L, N] in out_dtype (bf16, fp16 or fp32; by default bf16)."""
+    _input(a, "a", None, (torch.int8,))
+    _input(w, "w", a.device, (torch.int8,))
+    if a.dim() not in (2, 3) or w.dim() != 2 or w.shape[1] != a.shape[-1]:
+        raise ValueError(f"a must be [M, K] or [B, L, K] and w [N, K] (got {list(a.shape)} and {list(w.shape)})")
+    K, N = a.shape[-1], w.shape[0]
+    M = a.numel() // K if K else 0
+    if K < 1:
+        raise ValueError("K must be at least 1")
+    if (K > 1 and (a.stride(-1) != 1 or w.stride(1) != 1)) or \
+            (a.dim() == 3 and a.shape[0] > 1 and a.shape[1] > 1 and a.stride(0) != a.shape[1] * a.stride(1)):
+        raise ValueError("the rows of a and w must be contiguous, and those of a at one pitch")
+    pitch = a.stride(-2) if a.shape[-2] > 1 else a.stride(0)
+    _scales(a_scale, "a_scale", M, a.device)
+    _scales(w_scale, "w_scale", N, a.device)
+    if out is None:
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out has the unsupported type {out_dtype}")
+        out = torch.empty(*a.shape[:-1], N, device=a.device, dtype=out_dtype)
+    else:
+        _input(out, "out", a.device)
+        if out.shape != (*a.shape[:-1], N) or out_dtype not in (None, out.dtype) or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, {[*a.shape[:-1], N]} and of the type out_dtype")
+    p = _LinearArgs(M, N, K, a.data_ptr(), pitch, a_scale.data_ptr(), w.data_ptr(), w.stride(0), w_scale.data_ptr(), None, 0,
+                    out.data_ptr(), _DTYPES[out.dtype], N)
+    if bias is not None:
+        _input(bias, "bias", a.device)
+        if bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous [{N}] (got {list(bias.shape)})")
+        p.bias, p.bias_dtype = bias.data_ptr(), _DTYPES[bias.dtype]
+    if M and N:
+        _check(lib().sol_attn_quantized_linear(ctypes.byref(p), _stream(a.device)))
+    return out
+
+
+def linear_status(device=None, stream=None):
+    """Synchronises the stream and raises SolAttnError if a product on this device gave up a bounded wait."""
+    with torch.cuda.device(device if stream is None else stream.device):
+        _check(lib().sol_attn_linear_status(_stream(None) if stream is None else stream.cuda_stream))

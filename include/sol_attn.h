@@ -317,6 +317,32 @@ typedef struct sol_attn_rope_args {
  * Angles are formed in fp64. */
 int sol_attn_rope(const sol_attn_rope_args* args, void* stream);
 
+/* Arguments of sol_attn_quantized_linear.  Strides are in elements. */
+typedef struct sol_attn_linear_args {
+  int M, N, K;                   /* 1 <= K <= 131071: up to there the sums fit 32 bits */
+  const int8_t* a;               /* [M, K], 16-byte aligned, rows at multiples of 16 bytes */
+  long long a_stride;
+  const float* a_scale;          /* [M] */
+  const int8_t* w;               /* [N, K], 16-byte aligned, rows at multiples of 16 bytes */
+  long long w_stride;
+  const float* w_scale;          /* [N] */
+  const void* bias;              /* [N], NULL: none */
+  int bias_dtype;
+  void* out;                     /* [M, N], overlaps no input */
+  int out_dtype;
+  long long out_stride;
+} sol_attn_linear_args;
+
+/* Product of 8-bit integers with a scale for each token and each channel:
+ *   out[m, n] = (sum_k a[m, k] * w[n, k]) * a_scale[m] * w_scale[n] + bias[n]
+ * The sum is exact in 32-bit integers; the rest is fp32, rounded once. */
+int sol_attn_quantized_linear(const sol_attn_linear_args* args, void* stream);
+
+/* Status of the products enqueued on this device: synchronises stream and
+ * returns SOL_ATTN_OK, or SOL_ATTN_ERR_TIMEOUT (and clears the status) if a
+ * bounded wait of one of them gave up, whose output is then not valid. */
+int sol_attn_linear_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
