@@ -542,6 +542,52 @@ def run_all_configs(args):
         torch.cuda.empty_cache()
 
 
+def run_layer(args):
+    """Layer report (not a bench line): one AttentionLayer of the workload's
+    shape, its residual stream in fp32, and each of its operators alone (CUDA
+    events; the video shapes' tensors are larger than L2)."""
+    import torch
+
+    import block_sparse_attention_moments_b200 as sa
+    from synth import WORKLOADS
+    wl = WORKLOADS[args.workload]
+    L, H, d, C = wl.L, wl.H, wl.d, wl.H * wl.d
+    g = torch.Generator(device="cuda").manual_seed(wl.seed)
+    rnd = lambda *shape, std=1.0, dtype=torch.float32: torch.empty(shape, device="cuda", dtype=dtype).normal_(0, std, generator=g)
+    layer = sa.AttentionLayer(rnd(3 * C, C, std=C ** -0.5), rnd(C, C, std=C ** -0.5), H, b_qkv=rnd(3 * C, std=0.1),
+                              b_out=rnd(C, std=0.1), q_weight=torch.ones(C, device="cuda"),
+                              k_weight=torch.ones(C, device="cuda"))
+    x = rnd(1, L, C)
+    shift, scale, gate, next_shift, next_scale = rnd(1, 5, C, std=0.2).unbind(1)
+
+    def timed(fn):
+        for _ in range(args.warmup):
+            out = fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            out = fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / args.steps, out
+
+    ms = {}
+    ms["norm_modulate"], (h, hs) = timed(lambda: sa.norm_modulate(x, scale, shift, quantize=True))
+    ms["int8_linear_qkv"], qkv = timed(lambda: sa.int8_linear(h, hs, layer.w_qkv, layer.w_qkv_scale, layer.b_qkv))
+    qkv = qkv.view(1, L, 3, H, d)
+    ms["rope"], (q, k, v) = timed(lambda: sa.rope(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], grid=wl.grid, **layer.rope))
+    ms["forward"], o = timed(lambda: sa.forward(q, k, v, args.beta, wl.chunk))
+    ms["quantize_rows"], (o8, os_) = timed(lambda: sa.quantize_rows(o.transpose(1, 2)))
+    ms["int8_linear_out"], y = timed(lambda: sa.int8_linear(o8, os_, layer.w_out, layer.w_out_scale, layer.b_out))
+    ms["gate_residual_norm"], _ = timed(lambda: sa.gate_residual_norm(x, y, gate, next_scale, next_shift))
+    del h, hs, qkv, q, k, v, o, o8, os_, y
+    ms["layer"], _ = timed(lambda: layer(x, scale, shift, gate, beta=args.beta, chunk=wl.chunk, grid=wl.grid,
+                                         next_scale=next_scale, next_shift=next_shift))
+    sa.linear_status(x.device)
+    print(json.dumps({"mode": "layer", "workload": wl.name, "beta": args.beta, "tokens": L, "channels": C,
+                      "steps": args.steps, "ms": ms}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -577,6 +623,8 @@ def main():
     ap.add_argument("--configs", nargs="+", default=["wan", "hunyuan"])
     ap.add_argument("--routing-cost", action="store_true",
                     help="method's routing against a materialised top-k router (not a bench line)")
+    ap.add_argument("--layer", action="store_true",
+                    help="a whole attention layer of the workload's shape and its operators (not a bench line)")
     ap.add_argument("--role-profile", action="store_true",
                     help="run the profiling build (libsol_attn_profile.so) and print per-role cycle accounting")
     args = ap.parse_args()
@@ -584,6 +632,8 @@ def main():
         return run_role_profile(args)
     if args.routing_cost:
         return run_routing_cost(args)
+    if args.layer:
+        return run_layer(args)
     if args.all_configs:
         return run_all_configs(args)
     if args.ablation:

@@ -21,7 +21,7 @@ __all__ = [
     "forward", "stats", "forward_host", "stage_pool", "stage_threshold", "stage_fused",
     "workspace_bytes", "release", "kernels_per_forward", "DebugBuffers", "EXPORTED_SYMBOLS", "topk_route",
     "executed_flops", "BLOCK", "norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope",
-    "rope_axes", "int8_linear", "linear_status",
+    "rope_axes", "int8_linear", "linear_status", "AttentionLayer",
 ]
 
 FLAG_SELECT_ALL = 0x1
@@ -290,7 +290,7 @@ def executed_flops(selected_pairs: int, B: int, H: int, L: int, d: int, *, appro
 
 # The operators around the attention import torch, which this module does only where it is used.
 _LAYER_OPS = ("norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes",
-              "int8_linear", "linear_status")
+              "int8_linear", "linear_status", "AttentionLayer")
 
 
 def __getattr__(name):

@@ -17,10 +17,10 @@ import math
 
 import torch
 
-from . import _check, lib
+from . import _check, forward, lib
 
 __all__ = ["norm_modulate", "gate_residual", "gate_residual_norm", "quantize_rows", "rope", "rope_axes",
-           "int8_linear", "linear_status"]
+           "int8_linear", "linear_status", "AttentionLayer"]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -440,3 +440,54 @@ def linear_status(device=None, stream=None):
     """Synchronises the stream and raises SolAttnError if a product on this device gave up a bounded wait."""
     with torch.cuda.device(device if stream is None else stream.device):
         _check(lib().sol_attn_linear_status(_stream(None) if stream is None else stream.cuda_stream))
+
+
+# ------------------------------------------------------------------ the layer
+class AttentionLayer:
+    """The self-attention of a diffusion-transformer block around ``forward``, its two projections in 8-bit integers:
+
+      h        = norm(x) * (1 + scale) + shift, in 8 bits        norm_modulate
+      q, k, v  = h w_qkv^T + b_qkv                               int8_linear
+      q, k     : RMS norm, rotary positions; q, k, v head-major  rope
+      o        = sparse attention, in 8 bits token by token      forward, quantize_rows
+      y        = o w_out^T + b_out                               int8_linear
+      x', h'   = x + gate * y, norm(x') * (1 + next_scale) + next_shift   gate_residual_norm
+
+    w_qkv: [3 H d, C], the rows of q, k and v in that order; w_out: [C, H d]; b_qkv, b_out: their biases; C is the
+    width of x, d = 64 or 128.  Both are quantised here, once, row by row.  norm, eps, qk_norm, q_weight, k_weight,
+    pairing, theta and axes are those of norm_modulate and rope.  Forward only."""
+
+    def __init__(self, w_qkv, w_out, heads, *, b_qkv=None, b_out=None, norm="layer", eps=1e-6, qk_norm="token",
+                 q_weight=None, k_weight=None, pairing="interleaved", theta=10000.0, axes=None):
+        if w_qkv.dim() != 2 or w_out.dim() != 2 or heads < 1 or w_qkv.shape[0] % (3 * heads) or \
+                tuple(w_out.shape) != (w_qkv.shape[1], w_qkv.shape[0] // 3):
+            raise ValueError(f"w_qkv must be [3 H d, C] and w_out [C, H d] for {heads} heads "
+                             f"(got {list(w_qkv.shape)} and {list(w_out.shape)})")
+        self.heads, self.d = heads, w_qkv.shape[0] // (3 * heads)
+        if self.d not in (64, 128):
+            raise ValueError(f"a head must have 64 or 128 channels (got {self.d})")
+        self.w_qkv, self.w_qkv_scale = quantize_rows(w_qkv)
+        self.w_out, self.w_out_scale = quantize_rows(w_out)
+        self.b_qkv, self.b_out = b_qkv, b_out
+        self.norm, self.eps = norm, eps
+        self.rope = dict(norm=qk_norm, q_weight=q_weight, k_weight=k_weight, pairing=pairing, theta=theta, axes=axes,
+                         eps=eps)
+
+    def __call__(self, x, scale=None, shift=None, gate=None, *, beta, chunk, flags=0, grid=None, positions=None, start=0,
+                 next_scale=None, next_shift=None, x_out=None):
+        """x: [B, L, C], bf16 or fp32; scale, shift, gate, next_scale, next_shift: vectors as norm_modulate takes
+        them; beta, chunk, flags: the attention's; grid, positions, start: rope's.  Returns (x', h') with h' in
+        bf16; x_out=x updates the stream in place.  Runs on the current stream of x's device; the attention's
+        workspace is the device's, so calls on one device must not overlap."""
+        _input(x, "x", self.w_qkv.device, (torch.bfloat16, torch.float32))
+        if x.dim() != 3 or x.shape[2] != self.w_qkv.shape[1]:
+            raise ValueError(f"x must be [B, L, {self.w_qkv.shape[1]}] (got {list(x.shape)})")
+        B, L, _ = x.shape
+        with torch.cuda.device(x.device):
+            h, h_scale = norm_modulate(x, scale, shift, norm=self.norm, eps=self.eps, quantize=True)
+            qkv = int8_linear(h, h_scale, self.w_qkv, self.w_qkv_scale, self.b_qkv).view(B, L, 3, self.heads, self.d)
+            q, k, v = rope(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], grid=grid, positions=positions, start=start, **self.rope)
+            o = forward(q, k, v, beta, chunk, flags=flags)
+            o8, o_scale = quantize_rows(o.transpose(1, 2))
+            y = int8_linear(o8, o_scale, self.w_out, self.w_out_scale, self.b_out)
+            return gate_residual_norm(x, y, gate, next_scale, next_shift, norm=self.norm, eps=self.eps, x_out=x_out)

@@ -1,0 +1,129 @@
+"""A whole attention layer (AttentionLayer): its operators together, as they are used."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_sparse_attention_moments_b200 as sa  # noqa: E402
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def make(B, L, H, d, dtype, seed=0):
+    C = H * d
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *shape, std=1.0, mean=0.0, dtype=FP32: torch.empty(shape, device="cuda", dtype=dtype).normal_(mean, std, generator=g)
+    w = dict(w_qkv=rnd(3 * C, C, std=C ** -0.5), w_out=rnd(C, C, std=C ** -0.5), b_qkv=rnd(3 * C, std=0.1),
+             b_out=rnd(C, std=0.1), q_weight=rnd(C, mean=1, std=0.1), k_weight=rnd(C, mean=1, std=0.1))
+    vectors = [t for t in rnd(B, 5, C, std=0.3).unbind(1)]
+    return rnd(B, L, C, dtype=dtype), w, vectors
+
+
+def plain(x, w, vectors, H, grid, quantised):
+    """The layer in 64 bits with dense attention; quantised: its four 8-bit operands rounded as the layer rounds them."""
+    B, L, C = x.shape
+    d = C // H
+    shift, scale, gate, next_shift, next_scale = (v.double()[:, None] for v in vectors)
+
+    def eight(t):
+        if not quantised:
+            return t
+        s = t.abs().amax(-1, keepdim=True) / 127
+        return torch.round(t / s) * s
+
+    def norm(t):
+        c = t - t.mean(-1, keepdim=True)
+        return c / torch.sqrt((c * c).mean(-1, keepdim=True) + 1e-6)
+
+    def rms(t, weight):
+        return t / torch.sqrt((t * t).mean(-1, keepdim=True) + 1e-6) * weight.double()
+
+    x = x.double()
+    h = eight(norm(x) * (1 + scale) + shift)
+    q, k, v = (h @ eight(w["w_qkv"].double()).t() + w["b_qkv"].double()).chunk(3, -1)
+    f, r, c = grid
+    i = torch.arange(L, device="cuda")
+    pos = (torch.stack([i // (r * c), i // c % r, i % c], -1) * (i < f * r * c)[:, None]).double()
+    axes = sa.rope_axes(d)
+    t = torch.cat([pos[:, a, None] * torch.tensor([10000.0 ** (-2 * j / n) for j in range(n // 2)], device="cuda", dtype=torch.float64)
+                   for a, n in enumerate(axes)], -1)
+    turn = torch.polar(torch.ones_like(t), t)
+
+    def heads(u):
+        return u.view(B, L, H, d).transpose(1, 2)
+
+    def rotate(u):
+        return torch.view_as_real(torch.view_as_complex(heads(u).reshape(B, H, L, d // 2, 2)) * turn).flatten(-2)
+
+    q, k = rotate(rms(q, w["q_weight"])), rotate(rms(k, w["k_weight"]))
+    o = torch.softmax(q @ k.transpose(-1, -2) / math.sqrt(d), -1) @ heads(v)
+    y = eight(o.transpose(1, 2).flatten(2)) @ eight(w["w_out"].double()).t() + w["b_out"].double()
+    xn = x + gate * y
+    return xn, norm(xn) * (1 + next_scale) + next_shift, gate * y
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,L,H,d,grid,dtype", [(1, 1, 1, 64, (1, 1, 1), FP32), (2, 150, 3, 64, (2, 5, 13), FP32),
+                                                (1, 333, 2, 128, (3, 10, 11), BF16), (1, 640, 4, 128, (4, 10, 16), FP32)])
+def test_layer_against_the_formulas(B, L, H, d, grid, dtype):
+    """With every block selected, against dense attention in 64 bits on the same 8-bit weights and activations.
+    What the layer rounds besides: q, k, v, o and y to bf16 (2^-9 of the value each, root mean square 2^-9/sqrt(3) or
+    less), the attention's own probabilities to bf16, and 8-bit values that those roundings move across a half: an
+    operand that is off by the relative error e moves that many of its values by one step, which adds no more than e
+    again.  Five such steps in a row, each within 2^-8 of the whole in the 2-norm: 2 * 5 * 2^-8 = 4e-2 bounds the
+    block's own part gate * y, and h' is off by as much of its unit size, besides its own bf16."""
+    x, w, vectors = make(B, L, H, d, dtype)
+    layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], H, b_qkv=w["b_qkv"], b_out=w["b_out"], q_weight=w["q_weight"],
+                              k_weight=w["k_weight"])
+    shift, scale, gate, next_shift, next_scale = vectors
+    xn, h = layer(x, scale, shift, gate, beta=-math.inf, chunk=4, flags=sa.FLAG_SELECT_ALL, grid=grid,
+                  next_scale=next_scale, next_shift=next_shift)
+    assert xn.dtype == dtype and h.dtype == BF16
+    want_x, want_h, branch = plain(x, w, vectors, H, grid, True)
+    rounding = 2.0 ** -8 * want_x.norm() if dtype == BF16 else 0
+    assert (xn.double() - want_x).norm() <= 4e-2 * branch.norm() + rounding
+    assert (h.double() - want_h).norm() <= (4e-2 + 2.0 ** -7) * want_h.norm()
+
+
+@pytest.mark.gpu
+def test_layer_is_its_operators():
+    """The layer gives the bits of its operators called one by one, sparse, in place and over again."""
+    B, L, H, d, grid = 2, 700, 2, 128, (7, 10, 10)
+    x, w, vectors = make(B, L, H, d, BF16, 1)
+    shift, scale, gate, next_shift, next_scale = vectors
+    layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], H, b_qkv=w["b_qkv"], b_out=w["b_out"], q_weight=w["q_weight"],
+                              k_weight=w["k_weight"])
+    kw = dict(beta=0.5, chunk=8, grid=grid, next_scale=next_scale, next_shift=next_shift)
+    xn, h = layer(x, scale, shift, gate, **kw)
+    a, s = sa.norm_modulate(x, scale, shift, quantize=True)
+    wq, ws = sa.quantize_rows(w["w_qkv"])
+    qkv = sa.int8_linear(a, s, wq, ws, w["b_qkv"]).view(B, L, 3, H, d)
+    q, k, v = sa.rope(*qkv.unbind(2), grid=grid, norm="token", q_weight=w["q_weight"], k_weight=w["k_weight"])
+    o = sa.forward(q, k, v, 0.5, 8)
+    counts = sa.stats(B, H, L)
+    assert 0 < int(counts.sum()) < B * H * 11 * 11
+    a, s = sa.quantize_rows(o.transpose(1, 2))
+    wq, ws = sa.quantize_rows(w["w_out"])
+    y = sa.int8_linear(a, s, wq, ws, w["b_out"])
+    want = sa.gate_residual_norm(x, y, gate, next_scale, next_shift)
+    assert torch.equal(xn, want[0]) and torch.equal(h, want[1])
+    again = layer(x, scale, shift, gate, x_out=x, **kw)
+    assert again[0] is x and torch.equal(x, xn) and torch.equal(again[1], h)
+    sa.linear_status(x.device)
+
+
+@pytest.mark.gpu
+def test_refusals():
+    x, w, _ = make(1, 20, 2, 64, BF16)
+    with pytest.raises(ValueError, match="w_qkv must be"):
+        sa.AttentionLayer(w["w_qkv"], w["w_qkv"], 2)
+    with pytest.raises(ValueError, match="64 or 128"):
+        sa.AttentionLayer(w["w_qkv"], w["w_out"], 4)
+    layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], 2)
+    with pytest.raises(ValueError, match="x must be"):
+        layer(x[..., :64], beta=1.0, chunk=4, grid=(1, 4, 5))
+    with pytest.raises(ValueError, match="unsupported type"):
+        layer(x.half(), beta=1.0, chunk=4, grid=(1, 4, 5))
+    with pytest.raises(ValueError, match="grid or positions"):
+        layer(x, beta=1.0, chunk=4)
