@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <numeric>
 #include <type_traits>
 
 #include "host.h"
@@ -19,6 +20,8 @@ namespace {
 
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
+constexpr size_t kNormShared = 200 * 1024;   // shared memory for folded factors
+constexpr int kNormSharedRows = 32;           // rows of a block from which it folds them there
 constexpr int kRopeUnits = 2;   // units a thread holds: 16 warps reach H*d = 16384
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
@@ -72,12 +75,15 @@ bool rows_distinct(const Span& s) {
          (s.sb >= s.width && s.sl >= (s.B - 1) * s.sb + s.width);
 }
 
-bool vec16(const void* p, size_t size, std::initializer_list<long long> strides) {
-  if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+bool aligned(size_t to, const void* p, size_t size, std::initializer_list<long long> strides) {
+  if (reinterpret_cast<uintptr_t>(p) % to) return false;
   for (long long s : strides)
-    if (s * static_cast<long long>(size) % 16) return false;
+    if (s * static_cast<long long>(size) % static_cast<long long>(to)) return false;
   return true;
 }
+bool vec16(const void* p, size_t size, std::initializer_list<long long> strides) { return aligned(16, p, size, strides); }
+// Eight elements at a time: 16 bytes, or 32 of fp32.
+bool vec8(const void* p, size_t size, std::initializer_list<long long> strides) { return aligned(8 * size, p, size, strides); }
 
 int check_rows(const sol_attn_rows& r, const char* name, int B, int L) {
   if (!dtype_ok(r.dtype)) return fail(SOL_ATTN_ERR_ARG, "%s: unknown dtype %d", name, r.dtype);
@@ -106,26 +112,49 @@ int convert(const sol_attn_vectors& v, const char* name, int B, int L, Vectors* 
   return SOL_ATTN_OK;
 }
 
-template <typename TX, typename TY, bool RES>
-int launch_norm(const NormParams& p0, bool vec, int sms, cudaStream_t st) {
-  NormParams p = p0;
+template <typename TX, typename TY, int V, int N, bool RES, bool SHARED>
+int launch_norm_as(NormParams p, int dev, int sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.B) * p.L;
-  const int n = vec ? 4 : p.C <= 4096 ? 8 : 32;
-  const int per_warp = 32 * n * (vec ? 8 : 1);
+  const int per_warp = 32 * N * V;
   p.warps = (p.C + per_warp - 1) / per_warp;
-  const int teams = kNormThreads / 32 / p.warps;
-  const int threads = teams * p.warps * 32;
-  const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 2LL * sms));
-  if (vec) norm_kernel<TX, TY, 8, 4, RES><<<grid, threads, 0, st>>>(p);
-  else if (n == 8) norm_kernel<TX, TY, 1, 8, RES><<<grid, threads, 0, st>>>(p);
-  else norm_kernel<TX, TY, 1, 32, RES><<<grid, threads, 0, st>>>(p);
+  if constexpr (SHARED) {
+    const int teams = kNormThreads / 32 / p.warps;
+    const size_t smem = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
+    static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
+    if (!attr_set[dev]) {
+      CUDA_TRY(cudaFuncSetAttribute(norm_kernel<TX, TY, V, N, RES, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kNormShared)));
+      attr_set[dev] = true;
+    }
+    norm_kernel<TX, TY, V, N, RES, SHARED><<<sms, teams * p.warps * 32, smem, st>>>(p);
+  } else {
+    const int teams = std::max(1, 4 / p.warps);
+    const int threads = teams * p.warps * 32;
+    const int blocks = std::max(1, 1024 / threads) * sms;
+    const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, blocks));
+    norm_kernel<TX, TY, V, N, RES, SHARED><<<grid, threads, 0, st>>>(p);
+  }
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
 }
 
+template <typename TX, typename TY, bool RES>
+int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
+  const long long rows = static_cast<long long>(p.B) * p.L;
+  if (vec) {
+    const size_t smem = static_cast<size_t>(RES ? 4 : 2) * p.C * sizeof(float);
+    if (rows >= kNormSharedRows * static_cast<long long>(sms) && p.group >= kNormSharedRows && smem <= kNormShared)
+      return launch_norm_as<TX, TY, 8, 4, RES, true>(p, dev, sms, st);
+    if (p.C <= 8192) return launch_norm_as<TX, TY, 8, 2, RES, false>(p, dev, sms, st);
+    return launch_norm_as<TX, TY, 8, 4, RES, false>(p, dev, sms, st);
+  }
+  if (p.C <= 4096) return launch_norm_as<TX, TY, 1, 8, RES, false>(p, dev, sms, st);
+  return launch_norm_as<TX, TY, 1, 32, RES, false>(p, dev, sms, st);
+}
+
 template <typename TX, typename TY>
-int launch_norm_res(const NormParams& p, bool vec, int sms, cudaStream_t st) {
-  return p.y ? launch_norm<TX, TY, true>(p, vec, sms, st) : launch_norm<TX, TY, false>(p, vec, sms, st);
+int launch_norm_res(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
+  return p.y ? launch_norm<TX, TY, true>(p, vec, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, dev, sms, st);
 }
 
 template <typename T>
@@ -258,20 +287,20 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   p.x_sb = B > 1 ? a->x.stride_b : 0, p.x_sl = L > 1 ? a->x.stride_l : 0;
   p.x_inner = a->x_inner, p.x_sh = a->x_inner < C ? a->x_stride_h : 0;
   if (p.x_sh < 0) return fail(SOL_ATTN_ERR_ARG, "x has a negative stride");
-  bool vec = C % 8 == 0 && p.x_inner % 8 == 0 && vec16(p.x, xs, {p.x_sb, p.x_sl, p.x_sh});
+  bool vec = C % 8 == 0 && p.x_inner % 8 == 0 && vec8(p.x, xs, {p.x_sb, p.x_sl, p.x_sh});
   const Span x = span(p.x, xs, p.x_sb, p.x_sl, B, L, (C / p.x_inner - 1) * p.x_sh + p.x_inner);
   Span y{}, outs[3];
   int nouts = 0;
   if (a->y.data) {
     p.y = a->y.data, p.y_sb = B > 1 ? a->y.stride_b : 0, p.y_sl = L > 1 ? a->y.stride_l : 0;
-    vec = vec && vec16(p.y, ys, {p.y_sb, p.y_sl});
+    vec = vec && vec8(p.y, ys, {p.y_sb, p.y_sl});
     y = span(p.y, ys, p.y_sb, p.y_sl, B, L, C);
   }
   if (a->x_out.data) {
     if ((rc = check_rows(a->x_out, "x_out", B, L))) return rc;
     if (a->x_out.dtype != a->x.dtype) return fail(SOL_ATTN_ERR_UNSUPPORTED, "x_out must have the type of x");
     p.xo = a->x_out.data, p.xo_sb = B > 1 ? a->x_out.stride_b : 0, p.xo_sl = L > 1 ? a->x_out.stride_l : 0;
-    vec = vec && vec16(p.xo, xs, {p.xo_sb, p.xo_sl});
+    vec = vec && vec8(p.xo, xs, {p.xo_sb, p.xo_sl});
     const Span s = span(p.xo, xs, p.xo_sb, p.xo_sl, B, L, C);
     // in place: each row is read whole before it is written, by the same team
     const bool in_place = p.xo == p.x && p.xo_sb == p.x_sb && p.xo_sl == p.x_sl && p.x_inner == C;
@@ -283,7 +312,7 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   if (a->h.data) {
     if ((rc = check_rows(a->h, "h", B, L))) return rc;
     p.h = a->h.data, p.h_sb = B > 1 ? a->h.stride_b : 0, p.h_sl = L > 1 ? a->h.stride_l : 0;
-    vec = vec && vec16(p.h, ys, {p.h_sb, p.h_sl});
+    vec = vec && vec8(p.h, ys, {p.h_sb, p.h_sl});
     outs[nouts++] = span(p.h, ys, p.h_sb, p.h_sl, B, L, C);
     if (!rows_distinct(outs[nouts - 1])) return fail(SOL_ATTN_ERR_ARG, "rows of h share elements");
     if (overlap(outs[nouts - 1], x) || (p.y && overlap(outs[nouts - 1], y)))
@@ -307,6 +336,9 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
       (rc = convert(a->post_weight, "post_weight", B, L, &p.post_weight, &vec)) ||
       (rc = convert(a->post_bias, "post_bias", B, L, &p.post_bias, &vec)))
     return rc;
+  p.group = L;
+  for (const Vectors* v : {&p.scale, &p.shift, &p.gate})
+    if (v->p) p.group = std::gcd(p.group, v->per);
   p.rs = a->residual_scale;
   p.pre = a->norm, p.post = a->post_norm;
   p.pre_eps = a->eps, p.post_eps = a->post_eps;
@@ -314,11 +346,11 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, sms, st);
-  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, sms, st);
-  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, sms, st);
-  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, sms, st);
-  return launch_norm_res<float, float>(p, vec, sms, st);
+  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, dev, sms, st);
+  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, dev, sms, st);
+  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, dev, sms, st);
+  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, dev, sms, st);
+  return launch_norm_res<float, float>(p, vec, dev, sms, st);
 }
 
 int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
@@ -380,8 +412,8 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
     r.in = t.in, r.out = t.out;
     r.sb = B > 1 ? t.stride_b : 0, r.sl = L > 1 ? t.stride_l : 0, r.sh = H > 1 ? t.stride_h : 0;
     if (r.sb < 0 || r.sl < 0 || r.sh < 0) return fail(SOL_ATTN_ERR_ARG, "%s has a negative stride", names[i]);
-    if (!vec16(t.in, size, {r.sb, r.sl, r.sh}))
-      return fail(SOL_ATTN_ERR_ALIGN, "%s: strides must be multiples of 16 bytes", names[i]);
+    if (!vec8(t.in, size, {r.sb, r.sl, r.sh}) || !vec8(t.out, size, {}))
+      return fail(SOL_ATTN_ERR_ALIGN, "%s: base and strides must be multiples of 8 elements", names[i]);
     if (i < 2 && t.weight) {
       if (a->norm == kRopeNormNone) return fail(SOL_ATTN_ERR_ARG, "%s has a weight but no norm", names[i]);
       if (!dtype_ok(t.weight_dtype)) return fail(SOL_ATTN_ERR_ARG, "%s weight: unknown dtype %d", names[i], t.weight_dtype);

@@ -128,9 +128,9 @@ __device__ __forceinline__ void tmem_dealloc_all(uint32_t addr, uint32_t cols) {
 }
 
 __device__ __forceinline__ float bias_at(const LinearParams& p, int n) {
-  float f[1] = {0.f};
-  if (p.bias) load_param<1>(p.bias, p.bias_dtype, n, f);
-  return f[0];
+  float f[1][1] = {{0.f}};
+  if (p.bias) load_params<1, 1>(p.bias, p.bias_dtype, n, 0, 0, 1, f);
+  return f[0][0];
 }
 
 __device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int* m, int* n) {

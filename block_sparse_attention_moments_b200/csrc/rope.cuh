@@ -13,6 +13,8 @@
 // fp32: a position of 10^5 would cost an fp32 angle three of its digits.
 #pragma once
 
+#include <climits>
+
 #include "rows.cuh"
 
 namespace solattn {
@@ -205,19 +207,16 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
       for (int which = 0; which < 2; ++which) {
         const RopeTensor& x = which ? p.k : p.q;
         const float m = which ? mk : mq;
-        float a[8], e[8], w[8];
+        float a[8], e[8], w[2][8];
         widen(which ? rk[i].a : rq[i].a, a);
         widen(which ? rk[i].b : rq[i].b, e);
         if (p.norm != kRopeNormNone) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) a[j] *= m, e[j] *= m;
           if (x.weight) {
-            load_param<8>(x.weight, x.weight_dtype, wc, w);
+            load_params<8, 2>(x.weight, x.weight_dtype, 0, wc, second, INT_MAX, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] *= w[j];
-            load_param<8>(x.weight, x.weight_dtype, wc + second, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] *= w[j];
+            for (int j = 0; j < 8; ++j) a[j] *= w[0][j], e[j] *= w[1][j];
           }
         }
         rope_rotate(p.half, cs, sn, a, e);

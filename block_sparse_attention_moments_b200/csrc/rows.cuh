@@ -29,7 +29,7 @@ __device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x);
 template <>
 __device__ __forceinline__ float from_f32(float x) { return x; }
 
-// V elements as they lie in memory: V = 8 moves 16-byte vectors (two of them
+// V elements as they lie in memory: V = 8 moves 16-byte vectors (32-byte ones
 // for fp32), V = 1 single elements, for rows whose address or width is odd.
 template <typename T, int V>
 struct Raw;
@@ -54,10 +54,23 @@ __device__ __forceinline__ uint4 ld_row_v4(const void* p) {
                : "memory");
   return r;
 }
+// Eight fp32 in one 32-byte load (p 32-byte aligned): as two 16-byte loads each
+// of the warp's would fetch every 32-byte sector that it touches half of.
+__device__ __forceinline__ void ld_row_v8(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_row_v8(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 template <typename T>
 __device__ __forceinline__ void load_raw(Raw<T, 8>& v, const T* p) {
-#pragma unroll
-  for (int i = 0; i < Raw<T, 8>::kVecs; ++i) v.r[i] = ld_row_v4(reinterpret_cast<const uint4*>(p) + i);
+  if constexpr (sizeof(T) == 4) ld_row_v8(p, v.r[0], v.r[1]);
+  else v.r[0] = ld_row_v4(p);
 }
 template <typename T>
 __device__ __forceinline__ void load_raw(Raw<T, 1>& v, const T* p) {
@@ -114,12 +127,11 @@ __device__ __forceinline__ void widen(const Raw<T, 1>& v, float (&f)[1]) {
 
 template <typename T>
 __device__ __forceinline__ void store_row(T* p, const float (&f)[8]) {
-  uint4* q = reinterpret_cast<uint4*>(p);
   if constexpr (sizeof(T) == 4) {
-    q[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    q[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    st_row_v8(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])),
+              make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
   } else {
-    q[0] = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]), narrow2<T>(f[6], f[7]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]), narrow2<T>(f[6], f[7]));
   }
 }
 template <typename T>
@@ -127,28 +139,50 @@ __device__ __forceinline__ void store_row(T* p, const float (&f)[1]) {
   *p = from_f32<T>(f[0]);
 }
 
-// V consecutive elements of a vector of parameters whose type is only known at run time.
-template <int V>
-__device__ __forceinline__ void load_param(const void* p, int dtype, long long at, float (&f)[V]) {
-  if constexpr (V == 8) {
-    if (dtype == kDtypeFp32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-      const float4 a = q[0], b = q[1];
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// N vectors of V consecutive parameters, `step` elements apart, whose type is
+// only known at run time: one branch for all of them, so that the loads are
+// under way together.  Those at or past `end` are left as they are.
+template <int V, int N>
+__device__ __forceinline__ void load_params(const void* p, int dtype, long long at, int c, int step, int end,
+                                            float (&f)[N][V]) {
+  if (dtype == kDtypeFp32) {
+    const float* q = static_cast<const float*>(p) + at;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (dtype == kDtypeBf16) widen2<__nv_bfloat16>(w[i], f[2 * i], f[2 * i + 1]);
-        else widen2<__half>(w[i], f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < N; ++i) {
+      if (c + i * step >= end) continue;
+      if constexpr (V == 8) {
+        const float4 a = *reinterpret_cast<const float4*>(q + c + i * step);
+        const float4 b = *reinterpret_cast<const float4*>(q + c + i * step + 4);
+        f[i][0] = a.x, f[i][1] = a.y, f[i][2] = a.z, f[i][3] = a.w;
+        f[i][4] = b.x, f[i][5] = b.y, f[i][6] = b.z, f[i][7] = b.w;
+      } else {
+        f[i][0] = q[c + i * step];
       }
     }
   } else {
-    f[0] = dtype == kDtypeFp32   ? static_cast<const float*>(p)[at]
-           : dtype == kDtypeBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at])
-                                 : __half2float(static_cast<const __half*>(p)[at]);
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    const bool bf = dtype == kDtypeBf16;
+    uint4 w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (c + i * step >= end) continue;
+      if constexpr (V == 8) w[i] = *reinterpret_cast<const uint4*>(q + c + i * step);
+      else w[i].x = q[c + i * step];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (c + i * step >= end) continue;
+      if constexpr (V == 8) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (bf) widen2<__nv_bfloat16>(u[j], f[i][2 * j], f[i][2 * j + 1]);
+          else widen2<__half>(u[j], f[i][2 * j], f[i][2 * j + 1]);
+        }
+      } else {
+        f[i][0] = bf ? __uint_as_float(w[i].x << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(w[i].x)));
+      }
+    }
   }
 }
 

@@ -307,7 +307,7 @@ def rope(q, k, v=None, *, grid=None, positions=None, axes=None, start=0, theta=1
     """Rotary positions with several axes; returns (q, k) or (q, k, v), contiguous [B, H, L, d] as forward reads them.
 
     q, k, v: [B, L, H, d] of one type, such as views of one projection's [B, L, 3, H, d]; the channels of a head are
-    contiguous, other strides are multiples of 16 bytes, d is a multiple of 16.  v is only laid out anew.
+    contiguous, base address and other strides are multiples of 8 elements, d is a multiple of 16.  v is only laid out anew.
     Positions: grid=(frames, rows, columns) for tokens in raster order, the first one at raster index start (tokens
     behind the grid, such as text, do not turn); or positions [L, A] or [B, L, A] on the device, int32, int64,
     float32 or float64, with A axes of 1 to 4.  axes: channels of each axis, even numbers that sum to d (three axes:

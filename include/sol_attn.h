@@ -286,9 +286,10 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* args, void* stream);
 #define SOL_ATTN_POS_F64 4
 
 typedef struct sol_attn_rope_tensor {
-  const void* in;                /* [B, L, H, d], any strides that are multiples of 16 bytes */
+  const void* in;                /* [B, L, H, d]; base and strides are multiples of 8 elements */
   long long stride_b, stride_l, stride_h;
-  void* out;                     /* contiguous [B, H, L, d]; overlaps no input */
+  void* out;                     /* contiguous [B, H, L, d], aligned to 8 elements; overlaps no
+                                    input */
   const void* weight;            /* of the norm; NULL: ones */
   int weight_dtype;
 } sol_attn_rope_tensor;

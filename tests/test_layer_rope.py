@@ -266,7 +266,7 @@ def test_refusals():
     refused("goes with a norm", lambda: sa.rope(q, k, v, q_weight=torch.ones(64, device="cuda"), **kw))
     refused("contiguous", lambda: sa.rope(q, k, v, norm="head", k_weight=torch.ones(63, device="cuda"), **kw))
     refused("multiple of 16", lambda: sa.rope(q[..., :40], k[..., :40], axes=(8, 16, 16), **kw))
-    refused("16-byte|multiples of 16", lambda: sa.rope(q[..., 4:52], k[..., 4:52], axes=(16, 16, 16), **kw))
+    refused("16-byte|multiples of 8", lambda: sa.rope(q[..., 4:52], k[..., 4:52], axes=(16, 16, 16), **kw))
     refused("contiguous", lambda: sa.rope(q.transpose(2, 3), k.transpose(2, 3), axes=(0, 0, 2), **kw))
     refused("no backward", lambda: sa.rope(q.clone().requires_grad_(), k, v, **kw))
     refused("CUDA", lambda: sa.rope(q.cpu(), k, v, **kw))
