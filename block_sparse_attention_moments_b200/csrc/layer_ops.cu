@@ -20,9 +20,9 @@ namespace {
 
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
-constexpr size_t kNormShared = 200 * 1024;   // shared memory for folded factors
-constexpr int kNormSharedRows = 32;           // rows of a block from which it folds them there
-constexpr int kRopeUnits = 2;   // units a thread holds: 16 warps reach H*d = 16384
+constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
+constexpr int kNormRingRows = 32;                // rows of a block, and of a group, from which it is taken
+constexpr size_t kRopeShared = 220 * 1024;       // shared memory of the rotary kernel
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
 
@@ -112,44 +112,61 @@ int convert(const sol_attn_vectors& v, const char* name, int B, int L, Vectors* 
   return SOL_ATTN_OK;
 }
 
-template <typename TX, typename TY, int V, int N, bool RES, bool SHARED>
-int launch_norm_as(NormParams p, int dev, int sms, cudaStream_t st) {
+template <typename TX, typename TY, int V, int N, bool RES, int THREADS>
+int launch_norm_as(NormParams p, int sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.B) * p.L;
   const int per_warp = 32 * N * V;
   p.warps = (p.C + per_warp - 1) / per_warp;
-  if constexpr (SHARED) {
-    const int teams = kNormThreads / 32 / p.warps;
-    const size_t smem = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
-    static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
-    if (!attr_set[dev]) {
-      CUDA_TRY(cudaFuncSetAttribute(norm_kernel<TX, TY, V, N, RES, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kNormShared)));
-      attr_set[dev] = true;
-    }
-    norm_kernel<TX, TY, V, N, RES, SHARED><<<sms, teams * p.warps * 32, smem, st>>>(p);
-  } else {
-    const int teams = std::max(1, 4 / p.warps);
-    const int threads = teams * p.warps * 32;
-    const int blocks = std::max(1, 1024 / threads) * sms;
-    const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, blocks));
-    norm_kernel<TX, TY, V, N, RES, SHARED><<<grid, threads, 0, st>>>(p);
-  }
+  const int teams = std::max(1, 4 / p.warps);
+  const int threads = teams * p.warps * 32;
+  const int blocks = std::max(1, 1024 / threads) * sms;
+  const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, blocks));
+  norm_kernel<TX, TY, V, N, RES, THREADS><<<grid, threads, 0, st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
 }
 
+// Whether the call is one for the ring kernel; if it is, *rc is its status.
+template <typename TX, typename TY, bool RES, bool FULL>
+bool launch_norm_ring(NormParams p, int dev, int sms, cudaStream_t st, int* rc) {
+  constexpr int N = 4, THREADS = RES ? 640 : 800;
+  const long long rows = static_cast<long long>(p.B) * p.L;
+  const int per_warp = 32 * N * 8;
+  p.warps = (p.C + per_warp - 1) / per_warp;
+  if (FULL && p.C % per_warp) return launch_norm_ring<TX, TY, RES, false>(p, dev, sms, st, rc);
+  if (rows < kNormRingRows * static_cast<long long>(sms) || p.group < kNormRingRows || p.warps * 32 > THREADS) return false;
+  const int teams = p.warps > 1 ? std::min(15, THREADS / 32 / p.warps) : THREADS / 32;
+  const size_t factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
+  const size_t stage = static_cast<size_t>(teams) * p.warps * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
+  if (factors + stage > kNormRingShared) return false;
+  p.depth = static_cast<int>(std::min<size_t>(4, (kNormRingShared - factors) / stage));
+  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_ring_kernel<TX, TY, N, RES, FULL, THREADS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormRingShared));
+    if (e != cudaSuccess) {
+      *rc = fail(SOL_ATTN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      return true;
+    }
+    attr_set[dev] = true;
+  }
+  norm_ring_kernel<TX, TY, N, RES, FULL, THREADS><<<sms, teams * p.warps * 32, factors + p.depth * stage, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  *rc = e == cudaSuccess ? SOL_ATTN_OK : fail(SOL_ATTN_ERR_CUDA, "norm kernel: %s", cudaGetErrorString(e));
+  return true;
+}
+
 template <typename TX, typename TY, bool RES>
 int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
-  const long long rows = static_cast<long long>(p.B) * p.L;
+  int rc;
   if (vec) {
-    const size_t smem = static_cast<size_t>(RES ? 4 : 2) * p.C * sizeof(float);
-    if (rows >= kNormSharedRows * static_cast<long long>(sms) && p.group >= kNormSharedRows && smem <= kNormShared)
-      return launch_norm_as<TX, TY, 8, 4, RES, true>(p, dev, sms, st);
-    if (p.C <= 8192) return launch_norm_as<TX, TY, 8, 2, RES, false>(p, dev, sms, st);
-    return launch_norm_as<TX, TY, 8, 4, RES, false>(p, dev, sms, st);
+    if (launch_norm_ring<TX, TY, RES, true>(p, dev, sms, st, &rc)) return rc;
+    if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
+    return launch_norm_as<TX, TY, 8, 4, RES, 512>(p, sms, st);
   }
-  if (p.C <= 4096) return launch_norm_as<TX, TY, 1, 8, RES, false>(p, dev, sms, st);
-  return launch_norm_as<TX, TY, 1, 32, RES, false>(p, dev, sms, st);
+  if (p.C <= 2560) return launch_norm_as<TX, TY, 1, 4, RES, 640>(p, sms, st);
+  if (p.C <= 8192) return launch_norm_as<TX, TY, 1, 16, RES, 512>(p, sms, st);
+  return launch_norm_as<TX, TY, 1, 32, RES, 512>(p, sms, st);
 }
 
 template <typename TX, typename TY>
@@ -157,19 +174,43 @@ int launch_norm_res(const NormParams& p, bool vec, int dev, int sms, cudaStream_
   return p.y ? launch_norm<TX, TY, true>(p, vec, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, dev, sms, st);
 }
 
-template <typename T>
-int launch_rope(const RopeParams& p0, int sms, cudaStream_t st) {
-  RopeParams p = p0;
-  const int units = p.H * (p.d / 16);
-  p.warps = (units + 32 * kRopeUnits - 1) / (32 * kRopeUnits);
-  const size_t per_team = (p.d + (p.norm == kRopeNormHead ? 2 * units : 0)) * sizeof(float);
-  const int teams = std::max(1, std::min<int>(kRopeThreads / 32 / p.warps, static_cast<int>(40960 / per_team)));
+template <typename T, bool HALF>
+int launch_rope_as(RopeParams p, int dev, int sms, cudaStream_t st) {
+  constexpr int N = kRopeVectors / (HALF ? 2 : 1);
+  const int items = p.H * p.d / (HALF ? 16 : 8);
+  p.warps = (items + 32 * N - 1) / (32 * N);
+  const int group = p.d / (HALF ? 16 : 8);
+  p.by_lanes = 32 % group == 0;
+  // per team and parity: cosines and sines, and the items' sums where lanes cannot add them
+  p.team_floats = p.d + (p.norm == kRopeNormHead && !p.by_lanes ? (2 * items + 3) / 4 * 4 : 0);
+  const size_t tables = 2 * p.team_floats * sizeof(float), part = static_cast<size_t>(p.warps) * kRopeVectors * 32 * 8 * sizeof(T);
+  // the widest fp32 rows leave no room for v, and less than that for the weights of a token norm
+  p.staged = p.v.in && tables + 3 * part <= kRopeShared ? 3 : 2;
+  const size_t stage = p.staged * part, per_team = tables + stage;
+  size_t weights = p.norm == kRopeNormNone ? 0 : (p.norm == kRopeNormToken ? p.H : 1) * p.d * 2 * sizeof(float);
+  p.shared_weights = weights + per_team <= kRopeShared;
+  if (!p.shared_weights) weights = 0;
+  int teams = p.warps > 1 ? std::min(15, kRopeThreads / 32 / p.warps) : kRopeThreads / 32;
+  teams = std::max(1, std::min<int>(teams, static_cast<int>((kRopeShared - weights) / per_team)));
+  p.depth = 1;
+  while (p.depth < 4 && weights + teams * (per_team + p.depth * stage) <= kRopeShared) ++p.depth;
+  const size_t smem = weights + teams * (2 * p.team_floats * sizeof(float) + p.depth * stage);
+  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
+  if (!attr_set[dev]) {
+    CUDA_TRY(cudaFuncSetAttribute(rope_kernel<T, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(kRopeShared)));
+    attr_set[dev] = true;
+  }
   const long long tokens = static_cast<long long>(p.B) * p.L;
-  const int threads = teams * p.warps * 32;
-  const int grid = static_cast<int>(std::min<long long>((tokens + teams - 1) / teams, 2LL * sms));
-  rope_kernel<T, kRopeUnits><<<grid, threads, teams * per_team, st>>>(p);
+  const int grid = static_cast<int>(std::min<long long>((tokens + teams - 1) / teams, sms));
+  rope_kernel<T, HALF><<<grid, teams * p.warps * 32, smem, st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
+}
+
+template <typename T>
+int launch_rope(const RopeParams& p, int dev, int sms, cudaStream_t st) {
+  return p.half ? launch_rope_as<T, true>(p, dev, sms, st) : launch_rope_as<T, false>(p, dev, sms, st);
 }
 
 // 2-D map of rows of K elements (pitch in bytes) with a {box_k, box_rows} box
@@ -339,6 +380,7 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   p.group = L;
   for (const Vectors* v : {&p.scale, &p.shift, &p.gate})
     if (v->p) p.group = std::gcd(p.group, v->per);
+  p.channels = static_cast<float>(C), p.inv_channels = 1.f / p.channels;
   p.rs = a->residual_scale;
   p.pre = a->norm, p.post = a->post_norm;
   p.pre_eps = a->eps, p.post_eps = a->post_eps;
@@ -398,6 +440,7 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
   }
   p.B = B, p.L = L, p.H = H, p.d = d;
   p.norm = a->norm, p.eps = a->eps;
+  p.inv_channels = 1.f / static_cast<float>(p.norm == kRopeNormToken ? H * d : d);
   p.half = a->pairing == SOL_ATTN_PAIR_HALF;
   const size_t size = dtype_size(a->dtype);
   const long long n = static_cast<long long>(B) * H * L * d;
@@ -422,6 +465,11 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
     }
   }
   const int tensors = p.v.in ? 3 : 2;
+  p.packed = 1;
+  for (int i = 0; i < tensors; ++i) p.packed = p.packed && (out[i]->sh == d || H == 1);
+  // a head's place in the output is kept in 32 bits, by 8 elements
+  if (static_cast<long long>(H) * d / 8 * L > UINT_MAX)
+    return fail(SOL_ATTN_ERR_UNSUPPORTED, "H*L*d = %lld exceeds 2^35", static_cast<long long>(H) * d * L);
   for (int i = 0; i < tensors; ++i) {
     const char* o = static_cast<const char*>(out[i]->out);
     const char* o_end = o + n * static_cast<long long>(size);
@@ -438,9 +486,9 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->dtype == SOL_ATTN_BF16) return launch_rope<__nv_bfloat16>(p, sms, st);
-  if (a->dtype == SOL_ATTN_FP16) return launch_rope<__half>(p, sms, st);
-  return launch_rope<float>(p, sms, st);
+  if (a->dtype == SOL_ATTN_BF16) return launch_rope<__nv_bfloat16>(p, dev, sms, st);
+  if (a->dtype == SOL_ATTN_FP16) return launch_rope<__half>(p, dev, sms, st);
+  return launch_rope<float>(p, dev, sms, st);
 }
 
 int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {

@@ -20,6 +20,7 @@
 #pragma once
 
 #include "rows.cuh"
+#include "sm100_ptx.cuh"
 
 namespace solattn {
 
@@ -54,6 +55,8 @@ struct NormParams {
   Vectors scale, shift, gate, weight, bias, post_weight, post_bias;
   int warps;                      // warps of a team
   int group;                      // tokens that share all of their vectors
+  int depth;                      // stages of the ring
+  float channels, inv_channels;   // C and 1 / C
 };
 
 // The folded factors of N vectors of V channels, c, c + step, ...
@@ -129,245 +132,323 @@ __device__ __forceinline__ void get_factor(const float* plane, int nvec, int vec
 
 // Normalises a row that the team holds in registers (no weight or bias).
 template <int V, int N>
-__device__ __forceinline__ void normalise(Team& t, int kind, float eps, int C, const bool (&on)[N], float (&v)[N][V]) {
+__device__ __forceinline__ void normalise(Team& t, int kind, float eps, const NormParams& p, const bool (&on)[N], float (&v)[N][V]) {
   if (kind == kNormNone) return;
-  const float n = static_cast<float>(C);
   if (kind == kNormLayer) {
-    float s = 0.f;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum_v<V>(s, v[i]);   // zero outside the row
+    const float mean = divide_by(team_sum(t, s.x + s.y), p.channels, p.inv_channels);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += v[i][j];   // zero outside the row
-    const float mean = team_sum(t, s) / n;   // a division: the mean of equal values is that value
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = on[i] ? v[i][j] - mean : 0.f;
+      if (on[i]) add_s<V>(v[i], -mean);
   }
-  float s = 0.f;
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int i = 0; i < N; ++i) sum_sq<V>(s, v[i]);
+  const float r = rsqrtf(fmaf(team_sum(t, s.x + s.y), p.inv_channels, eps));
 #pragma unroll
-    for (int j = 0; j < V; ++j) s = fmaf(v[i][j], v[i][j], s);
-  const float r = rsqrtf(team_sum(t, s) / n + eps);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[i][j] *= r;
+  for (int i = 0; i < N; ++i) mul_s<V>(v[i], r);
 }
 
-constexpr int kNormThreads = 512;
-
-// One team to a row; thread t of the team holds the row's vectors t, t + T,
-// t + 2T, ... (T threads, N vectors of V elements at most).  A team goes
-// through consecutive rows, or through every teams-th row of its block's
-// share, and asks for its next row as soon as it has taken the present one
-// out of the load registers, before that row's sums.
-//
-// SHARED: the block folds the factors of a modulation group into shared memory
-// and its teams read them from there; else every thread keeps those of its own
-// channels in registers and folds them anew where the group changes.
-template <typename TX, typename TY, int V, int N, bool RES, bool SHARED>
-__global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const __grid_constant__ NormParams p) {
-  extern __shared__ __align__(16) float factors[];
-  __shared__ float slots[2 * (kNormThreads / 32)];
-  Team team;
-  team.warps = p.warps;
-  team.index = (threadIdx.x / 32) / p.warps;
-  team.warp = (threadIdx.x / 32) % p.warps;
-  team.slots = slots + 2 * p.warps * team.index;
-  team.turn = 0;
-  const int teams = blockDim.x / 32 / p.warps;
-  const int T = p.warps * 32;
-  const int tid = threadIdx.x - team.index * T;
-  const int nvec = p.C / V;
-  const long long rows = static_cast<long long>(p.B) * p.L;
-
-  bool on[N];
+// What happens to a row v = x' (unrounded) of a team: x' is written, normed,
+// modulated with the factors that pre(i, a, c) gives, and written as h and in
+// 8 bits.
+template <typename TX, typename TY, int V, int N, bool RES, class Pre>
+__device__ __forceinline__ void emit_row(const NormParams& p, Team& team, unsigned row, int b, int l, int first,
+                                         const bool (&on)[N], float (&v)[N][V], Pre pre) {
+  if constexpr (RES) {
+    if (p.xo) {
+      TX* op = static_cast<TX*>(p.xo) + b * p.xo_sb + l * p.xo_sl;
 #pragma unroll
-  for (int i = 0; i < N; ++i) on[i] = tid + i * T < nvec;
-
-  // this block's rows (SHARED) or this team's
-  const long long parts = SHARED ? gridDim.x : static_cast<long long>(gridDim.x) * teams;
-  const long long part = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * teams + team.index;
-  const long long begin = rows * part / parts, end = rows * (part + 1) / parts;
-
-  float A[SHARED ? 1 : N][V], Bv[SHARED ? 1 : N][V];        // of pre
-  float PA[SHARED || !RES ? 1 : N][V], PB[SHARED || !RES ? 1 : N][V];   // of post and gate
-  Raw<TX, V> rx[N];
-  Raw<TY, V> ry[RES ? N : 1];
-  auto load = [&](long long row) {
-    const int b = static_cast<int>(row / p.L);
-    const int l = static_cast<int>(row - static_cast<long long>(b) * p.L);
-    const TX* xp = static_cast<const TX*>(p.x) + b * p.x_sb + l * p.x_sl;
+      for (int i = 0; i < N; ++i)
+        if (on[i]) store_row(op + (first + i * 32) * V, v[i]);
+    }
+    if (!p.h && !p.q) return;
+  }
+  normalise<V, N>(team, p.pre, p.pre_eps, p, on, v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!on[i]) continue;
+    float a[V], c[V];
+    pre(i, a, c);
+    fma_v<V>(v[i], v[i], a, c);
+  }
+  if (p.h) {
+    TY* hp = static_cast<TY*>(p.h) + b * p.h_sb + l * p.h_sl;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) store_row(hp + (first + i * 32) * V, v[i]);
+  }
+  if (p.q) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (on[i]) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+    const float amax = __uint_as_float(team_max(team, m));
+    // q = h * (127 / amax).  A row of zeros has the scale 0; of one with an
+    // infinity or a NaN the scale is not finite.  Both get the factor 0, and
+    // what is NaN then becomes 0 as a whole number.  Below 2^-120 the row is
+    // scaled up first, as 127 / amax would overflow.
+    const bool tiny = amax < 0x1p-120f;
+    if (tiny) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) mul_s<V>(v[i], 0x1p100f);
+    }
+    const float up = amax > 0.f && amax <= 3.402823466e38f ? 127.f / (tiny ? amax * 0x1p100f : amax) : 0.f;
+    int8_t* qp = p.q + row * p.q_sl;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!on[i]) continue;
-      const int c = (tid + i * T) * V;
-      load_raw(rx[i], xp + (p.x_inner == p.C ? c : (c / p.x_inner) * p.x_sh + c % p.x_inner));
+      mul_s<V>(v[i], up);
+      if constexpr (V == 8) {
+        int k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = __float2int_rn(v[i][j]);
+        *reinterpret_cast<uint2*>(qp + (first + i * 32) * 8) =
+            make_uint2(pack_s8(k[0], k[1], k[2], k[3]), pack_s8(k[4], k[5], k[6], k[7]));
+      } else {
+        qp[first + i * 32] = static_cast<int8_t>(__float2int_rn(v[i][0]));
+      }
+    }
+    if (first == 0) p.q_scale[row] = amax / 127.f;
+  }
+}
+
+// Few rows, short groups, rows that vectors cannot read.  One team to a row;
+// each warp has 32 N consecutive vectors of V elements, each thread N of them
+// and, in registers, the folded factors of its channels, which it folds anew
+// where the group changes.  A
+// team goes through consecutive rows and asks for the next one as soon as it
+// has taken the present one out of the load registers, before its sums.
+template <typename TX, typename TY, int V, int N, bool RES, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ __align__(16) float slots[team_slots(THREADS, 1)];
+  Team team;
+  make_team<1>(team, p.warps, slots, team_slots(THREADS, 1));
+  const int teams = blockDim.x / 32 / p.warps;
+  const int first = team.warp * 32 * N + threadIdx.x % 32;   // this thread's vectors: first, first + 32, ...
+  const int nvec = p.C / V;
+  const unsigned L = p.L, rows = p.B * L;   // below 2^31
+
+  bool on[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) on[i] = first + i * 32 < nvec;
+
+  const unsigned long long parts = gridDim.x * teams, part = blockIdx.x * teams + team.index;
+  const unsigned begin = rows * part / parts, end = rows * (part + 1) / parts;
+
+  float A[N][V], Bv[N][V];                            // of pre
+  float PA[RES ? N : 1][V], PB[RES ? N : 1][V];       // of post and gate
+  Raw<TX, V> rx[N];
+  Raw<TY, V> ry[RES ? N : 1];
+  auto load = [&](unsigned row) {
+    const int b = row / L;
+    const int l = row - b * L;
+    const TX* xp = static_cast<const TX*>(p.x) + b * p.x_sb + l * p.x_sl;
+    if (p.x_inner == p.C) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (on[i]) load_raw(rx[i], xp + (first + i * 32) * V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (first + i * 32) * V;
+        if (on[i]) load_raw(rx[i], xp + (c / p.x_inner) * p.x_sh + c % p.x_inner);
+      }
     }
     if constexpr (RES) {
       const TY* yp = static_cast<const TY*>(p.y) + b * p.y_sb + l * p.y_sl;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (on[i]) load_raw(ry[i], yp + (tid + i * T) * V);
+        if (on[i]) load_raw(ry[i], yp + (first + i * 32) * V);
     }
   };
 
-  auto do_row = [&](long long row, int b, int l, long long next) {
+  if (begin < end) load(begin);
+  __syncthreads();   // the team's slots are clear
+  int until = 0, of = -1;   // the factors hold for the tokens below `until` of batch element `of`
+  for (unsigned row = begin; row < end; ++row) {
+    const int b = row / L;
+    const int l = row - b * L;
+    if (b != of || l >= until) {
+      fold_pre<V, N>(p, b, l, first * V, 32 * V, A, Bv);
+      if constexpr (RES) fold_post<V, N>(p, b, l, first * V, 32 * V, PA, PB);
+      of = b;
+      until = l - l % p.group + p.group;
+    }
     float v[N][V];
-    if constexpr (RES) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (on[i]) widen(ry[i], v[i]);
-        else
-#pragma unroll
-          for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      }
-      normalise<V, N>(team, p.post, p.post_eps, p.C, on, v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float x[V], a[V], c[V];
-        if (!on[i]) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-          continue;
-        }
-        widen(rx[i], x);
-        if constexpr (SHARED) {
-          get_factor<V>(factors + 2 * p.C, nvec, tid + i * T, a);
-          if (p.post_bias.p) get_factor<V>(factors + 3 * p.C, nvec, tid + i * T, c);
-          else
-#pragma unroll
-            for (int j = 0; j < V; ++j) c[j] = 0.f;
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) a[j] = PA[i][j], c[j] = PB[i][j];
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = fmaf(p.rs, x[j], fmaf(v[i][j], a[j], c[j]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (on[i]) widen(rx[i], v[i]);
-        else
-#pragma unroll
-          for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      }
-    }
-    if (next < end) load(next);
-    if constexpr (RES) {
-      if (p.xo) {
-        TX* op = static_cast<TX*>(p.xo) + b * p.xo_sb + l * p.xo_sl;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (on[i]) store_row(op + (tid + i * T) * V, v[i]);
-      }
-      if (!p.h && !p.q) return;
-    }
-    normalise<V, N>(team, p.pre, p.pre_eps, p.C, on, v);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (!on[i]) continue;
-      float a[V], c[V];
-      if constexpr (SHARED) {
-        get_factor<V>(factors, nvec, tid + i * T, a);
-        get_factor<V>(factors + p.C, nvec, tid + i * T, c);
+      if (on[i]) {
+        if constexpr (RES) widen(ry[i], v[i]);
+        else widen(rx[i], v[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) a[j] = A[i][j], c[j] = Bv[i][j];
+        for (int j = 0; j < V; ++j) v[i][j] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = fmaf(v[i][j], a[j], c[j]);
     }
-    if (p.h) {
-      TY* hp = static_cast<TY*>(p.h) + b * p.h_sb + l * p.h_sl;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (on[i]) store_row(hp + (tid + i * T) * V, v[i]);
-    }
-    if (p.q) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (on[i]) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-      const float amax = __uint_as_float(team_max(team, m));
-      // a row of zeros: scale 0 and zeros; a row with an infinity or a NaN:
-      // a scale that is not finite and zeros, so that what is made of it is NaN
-      const bool plain = amax > 0.f && amax <= 3.402823466e38f;
-      // h / s as h * (127 / amax) (an amax below 127 / FLT_MAX would overflow
-      // the quotient; there the division itself is taken)
-      const float up = 127.f / amax;
-      const float s = amax / 127.f;
-      const bool tiny = plain && !(up <= 3.402823466e38f);
-      int8_t* qp = p.q + row * p.q_sl;
+    if constexpr (RES) {
+      normalise<V, N>(team, p.post, p.post_eps, p, on, v);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (!on[i]) continue;
-        int k[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float u = tiny ? (v[i][j] / amax) * 127.f : v[i][j] * up;
-          k[j] = plain ? max(-127, min(127, __float2int_rn(u))) : 0;
-        }
-        if constexpr (V == 8) {
-          uint2 w;
-          w.x = (k[0] & 255) | (k[1] & 255) << 8 | (k[2] & 255) << 16 | static_cast<uint32_t>(k[3]) << 24;
-          w.y = (k[4] & 255) | (k[5] & 255) << 8 | (k[6] & 255) << 16 | static_cast<uint32_t>(k[7]) << 24;
-          *reinterpret_cast<uint2*>(qp + (tid + i * T) * 8) = w;
-        } else {
-          qp[tid + i * T] = static_cast<int8_t>(k[0]);
-        }
+        float x[V];
+        widen(rx[i], x);
+        fma_v<V>(v[i], v[i], PA[i], PB[i]);
+        fma_s<V>(v[i], x, p.rs, v[i]);
       }
-      if (tid == 0) p.q_scale[row] = s;
     }
+    if (row + 1 < end) load(row + 1);
+    emit_row<TX, TY, V, N, RES>(p, team, row, b, l, first, on, v, [&](int i, float(&a)[V], float(&c)[V]) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) a[j] = A[i][j], c[j] = Bv[i][j];
+    });
+  }
+}
+
+// Many rows of long groups.  The block folds the factors of a group into
+// shared memory and its teams, each with every teams-th row of the block's
+// share, read them from there.  Rows come through a ring of p.depth stages in
+// shared memory by asynchronous copies, each warp's part by that warp: rows on
+// their way cost no registers, and no barrier but the warp's own.
+template <typename TX, typename TY, int N, bool RES, bool FULL, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const __grid_constant__ NormParams p) {
+  constexpr int V = 8;
+  constexpr int kX = N * 32 * V * sizeof(TX), kY = RES ? N * 32 * V * sizeof(TY) : 0;   // bytes of a warp's stage
+  extern __shared__ __align__(16) float factors[];
+  __shared__ __align__(16) float slots[team_slots(THREADS, 1)];
+  Team team;
+  make_team<1>(team, p.warps, slots, team_slots(THREADS, 1));
+  const int lane = threadIdx.x % 32;
+  const int teams = blockDim.x / 32 / p.warps;
+  const int first = team.warp * 32 * N + threadIdx.x % 32;   // this thread's vectors: first, first + 32, ...
+  const int nvec = p.C / V;
+  const unsigned L = p.L, rows = p.B * L;   // below 2^31
+  const int planes = RES ? (p.post_bias.p ? 4 : 3) : 2;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(factors + planes * p.C) + (threadIdx.x / 32) * p.depth * (kX + kY);
+
+  bool on[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) on[i] = first + i * 32 < nvec;
+
+  const unsigned begin = static_cast<unsigned long long>(rows) * blockIdx.x / gridDim.x;
+  const unsigned end = static_cast<unsigned long long>(rows) * (blockIdx.x + 1) / gridDim.x;
+
+  constexpr int kPieceX = 16 / sizeof(TX), kPieceY = 16 / sizeof(TY);   // channels of a 16-byte piece
+  const int c0 = team.warp * 32 * N * V;                                // the warp's first channel
+  // the row that the next copies bring: batch element, token, and whether it is the block's
+  unsigned next = begin + team.index;
+  int nb = next / L, nl = next - nb * L;
+  auto load = [&](int stage) {
+    if (next < end) {
+      const uint32_t dst = smem_u32(ring + stage * (kX + kY)) + lane * 16;
+      const TX* xp = static_cast<const TX*>(p.x) + nb * p.x_sb + nl * p.x_sl;
+      if (p.x_inner == p.C) {
+        const TX* xl = xp + c0 + lane * kPieceX;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int h = 0; h < V / kPieceX; ++h)
+            if (FULL || c0 + i * 32 * V + (lane + 32 * h) * kPieceX < p.C)
+              cp_async_16(dst + i * 32 * V * sizeof(TX) + 512 * h, xl + i * 32 * V + 32 * h * kPieceX);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int h = 0; h < V / kPieceX; ++h) {
+            const int c = c0 + i * 32 * V + (lane + 32 * h) * kPieceX;
+            if (FULL || c < p.C)
+              cp_async_16(dst + i * 32 * V * sizeof(TX) + 512 * h, xp + (c / p.x_inner) * p.x_sh + c % p.x_inner);
+          }
+      }
+      if constexpr (RES) {
+        const TY* yl = static_cast<const TY*>(p.y) + nb * p.y_sb + nl * p.y_sl + c0 + lane * kPieceY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int h = 0; h < V / kPieceY; ++h)
+            if (FULL || c0 + i * 32 * V + (lane + 32 * h) * kPieceY < p.C)
+              cp_async_16(dst + kX + i * 32 * V * sizeof(TY) + 512 * h, yl + i * 32 * V + 32 * h * kPieceY);
+      }
+      next += teams;
+      nl += teams;
+      while (nl >= p.L) nl -= p.L, ++nb;
+    }
+    cp_async_commit();   // also where there is nothing to copy: groups are counted
   };
 
-  if constexpr (SHARED) {
-    long long have = -1;   // the row in the load registers
-    for (long long s0 = begin; s0 < end;) {
-      const int b = static_cast<int>(s0 / p.L);
-      const int l = static_cast<int>(s0 - static_cast<long long>(b) * p.L);
-      const long long s1 = min(end, s0 + (p.group - l % p.group));   // the group's end
-      if (s0 + team.index < s1 && have != s0 + team.index) load(have = s0 + team.index);
-      __syncthreads();   // the factors of the group before have been read
-      for (int vec = threadIdx.x; vec < nvec; vec += blockDim.x) {
-        float a[1][V], c[1][V];
-        fold_pre<V, 1>(p, b, l, vec * V, 0, a, c);
-        put_factor<V>(factors, nvec, vec, a[0]);
-        put_factor<V>(factors + p.C, nvec, vec, c[0]);
-        if constexpr (RES) {
-          fold_post<V, 1>(p, b, l, vec * V, 0, a, c);
-          put_factor<V>(factors + 2 * p.C, nvec, vec, a[0]);
-          if (p.post_bias.p) put_factor<V>(factors + 3 * p.C, nvec, vec, c[0]);
+  unsigned row = begin + team.index;
+  for (int s = 0; s < p.depth; ++s) load(s);
+  int stage = 0;
+  for (unsigned s0 = begin; s0 < end;) {
+    const int b = s0 / L;
+    const int l0 = s0 - b * L;
+    const unsigned s1 = min(end, s0 + (p.group - l0 % p.group));   // the group's end
+    __syncthreads();   // the factors of the group before have been read
+    for (int vec = threadIdx.x; vec < nvec; vec += blockDim.x) {
+      float a[1][V], c[1][V];
+      fold_pre<V, 1>(p, b, l0, vec * V, 0, a, c);
+      put_factor<V>(factors, nvec, vec, a[0]);
+      put_factor<V>(factors + p.C, nvec, vec, c[0]);
+      if constexpr (RES) {
+        fold_post<V, 1>(p, b, l0, vec * V, 0, a, c);
+        put_factor<V>(factors + 2 * p.C, nvec, vec, a[0]);
+        if (p.post_bias.p) put_factor<V>(factors + 3 * p.C, nvec, vec, c[0]);
+      }
+    }
+    __syncthreads();
+    for (; row < s1; row += teams) {
+      // all but the depth - 1 youngest groups are complete: this row has come
+      if (p.depth == 1) cp_async_wait<0>();
+      else if (p.depth == 2) cp_async_wait<1>();
+      else if (p.depth == 3) cp_async_wait<2>();
+      else cp_async_wait<3>();
+      __syncwarp();
+      const uint8_t* src = ring + stage * (kX + kY);
+      float v[N][V];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (on[i]) {
+          if constexpr (RES) take_staged<TY>(src + kX, i * 32 + lane, v[i]);
+          else take_staged<TX>(src, i * 32 + lane, v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[i][j] = 0.f;
         }
       }
-      __syncthreads();
-      for (long long row = s0 + team.index; row < s1; row += teams) {
-        if (have != row) load(row);
-        have = row + teams < s1 ? row + teams : s1 + team.index;
-        do_row(row, b, l + static_cast<int>(row - s0), have);
+      if constexpr (RES) {
+        normalise<V, N>(team, p.post, p.post_eps, p, on, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (!on[i]) continue;
+          float x[V], a[V];
+          get_factor<V>(factors + 2 * p.C, nvec, first + i * 32, a);
+          if (p.post_bias.p) {
+            float c[V];
+            get_factor<V>(factors + 3 * p.C, nvec, first + i * 32, c);
+            fma_v<V>(v[i], v[i], a, c);
+          } else {
+            mul_v<V>(v[i], a);
+          }
+          take_staged<TX>(src, i * 32 + lane, x);
+          fma_s<V>(v[i], x, p.rs, v[i]);
+        }
       }
-      s0 = s1;
+      __syncwarp();   // all lanes have read the stage
+      load(stage);
+      stage = stage + 1 == p.depth ? 0 : stage + 1;
+      emit_row<TX, TY, V, N, RES>(p, team, row, b, l0 + (row - s0), first, on, v,
+                                  [&](int i, float(&a)[V], float(&c)[V]) {
+                                    get_factor<V>(factors, nvec, first + i * 32, a);
+                                    get_factor<V>(factors + p.C, nvec, first + i * 32, c);
+                                  });
     }
-  } else {
-    if (begin < end) load(begin);
-    int until = 0, of = -1;   // the factors hold for the tokens below `until` of batch element `of`
-    for (long long row = begin; row < end; ++row) {
-      const int b = static_cast<int>(row / p.L);
-      const int l = static_cast<int>(row - static_cast<long long>(b) * p.L);
-      if (b != of || l >= until) {
-        fold_pre<V, N>(p, b, l, tid * V, T * V, A, Bv);
-        if constexpr (RES) fold_post<V, N>(p, b, l, tid * V, T * V, PA, PB);
-        of = b;
-        until = l - l % p.group + p.group;
-      }
-      do_row(row, b, l, row + 1);
-    }
+    s0 = s1;
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace solattn

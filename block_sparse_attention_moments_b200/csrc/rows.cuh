@@ -77,6 +77,18 @@ __device__ __forceinline__ void load_raw(Raw<T, 1>& v, const T* p) {
   v.r = *p;
 }
 
+// A warp's asynchronous copy of 32 consecutive vectors of 8 elements (those of
+// lanes with on[i]) into its own shared memory, and their way out of it.  The
+// copies go by 16-byte pieces in address order; a lane of fp32 finds its 32
+// bytes in pieces that two other lanes have copied, so it reads behind a
+// __syncwarp and the warp refills behind another.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int D>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D) : "memory"); }
+
 template <typename T>
 __device__ __forceinline__ void widen2(uint32_t w, float& a, float& b);
 template <>
@@ -120,6 +132,15 @@ __device__ __forceinline__ void widen(const Raw<T, 8>& v, float (&f)[8]) {
     widen2<T>(v.r[0].w, f[6], f[7]);
   }
 }
+// Vector `vec` of a stage that asynchronous copies have filled.
+template <typename T>
+__device__ __forceinline__ void take_staged(const uint8_t* stage, int vec, float (&f)[8]) {
+  Raw<T, 8> r;
+#pragma unroll
+  for (int h = 0; h < Raw<T, 8>::kVecs; ++h)
+    r.r[h] = *reinterpret_cast<const uint4*>(stage + vec * 8 * static_cast<int>(sizeof(T)) + 16 * h);
+  widen(r, f);
+}
 template <typename T>
 __device__ __forceinline__ void widen(const Raw<T, 1>& v, float (&f)[1]) {
   f[0] = to_f32<T>(v.r);
@@ -135,8 +156,99 @@ __device__ __forceinline__ void store_row(T* p, const float (&f)[8]) {
   }
 }
 template <typename T>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, 8>& v) {
+  if constexpr (sizeof(T) == 4) st_row_v8(p, v.r[0], v.r[1]);
+  else *reinterpret_cast<uint4*>(p) = v.r[0];
+}
+template <typename T>
 __device__ __forceinline__ void store_row(T* p, const float (&f)[1]) {
   *p = from_f32<T>(f[0]);
+}
+
+// ------------------------------------------------------------------ arithmetic on V values
+// Two fp32 operations an instruction where V is even.
+template <int V>
+__device__ __forceinline__ void fma_v(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), make_float2(c[j], c[j + 1]));
+      d[j] = r.x, d[j + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = fmaf(a[j], b[j], c[j]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void fma_s(float (&d)[V], const float (&a)[V], float b, const float (&c)[V]) {
+  float t[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) t[j] = b;
+  fma_v<V>(d, a, t, c);
+}
+template <int V>
+__device__ __forceinline__ void mul_v(float (&d)[V], const float (&a)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 r = __fmul2_rn(make_float2(d[j], d[j + 1]), make_float2(a[j], a[j + 1]));
+      d[j] = r.x, d[j + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] *= a[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void mul_s(float (&d)[V], float a) {
+  float t[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) t[j] = a;
+  mul_v<V>(d, t);
+}
+template <int V>
+__device__ __forceinline__ void add_s(float (&d)[V], float a) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 r = __fadd2_rn(make_float2(d[j], d[j + 1]), make_float2(a, a));
+      d[j] = r.x, d[j + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] += a;
+  }
+}
+// Adds the values, or their squares, to two partial sums.
+template <int V>
+__device__ __forceinline__ void sum_v(float2& s, const float (&a)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) s = __fadd2_rn(s, make_float2(a[j], a[j + 1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s.x += a[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void sum_sq(float2& s, const float (&a)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) s = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(a[j], a[j + 1]), s);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s.x = fmaf(a[j], a[j], s.x);
+  }
+}
+
+// Four values, each within the range, as s8 (the first in the lowest byte).
+__device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(b), "r"(c), "r"(d));
+  return r;
 }
 
 // N vectors of V consecutive parameters, `step` elements apart, whose type is
@@ -190,13 +302,34 @@ __device__ __forceinline__ void load_params(const void* p, int dtype, long long 
 // A team is `warps` whole warps of a block, numbered from 0; a block holds up
 // to 15 teams of more than one warp (each has a named barrier of its own,
 // barrier 0 being the block's).  Every warp of a team takes the same calls.
+// Its warps meet in two rows of `padded` slots of W floats, which alternate:
+// one barrier a reduction is enough then, as a warp that is one reduction
+// ahead writes the other row, and it cannot be two ahead.  Slots past the last
+// warp's stay zero, so that four are read at a time.
 struct Team {
   int warps;      // warps of a team
   int index;      // this team's number in the block
   int warp;       // this warp's number in the team
-  float* slots;   // shared memory, 2 * warps floats of this team
-  int turn;       // which half of the slots the next reduction writes
+  int padded;     // warps, rounded up to four
+  float* slots;   // the row that the next reduction writes
+  float* other;
 };
+
+// Shared floats of a block of `threads` threads for reductions of W values.
+constexpr int team_slots(int threads, int W) { return 4 * W * (threads / 32) + 16; }
+
+// The slots (16-byte aligned, team_slots() of them) are cleared here: the
+// caller has the block synchronise before the first reduction.
+template <int W>
+__device__ __forceinline__ void make_team(Team& t, int warps, float* slots, int count) {
+  t.warps = warps;
+  t.index = (threadIdx.x / 32) / warps;
+  t.warp = (threadIdx.x / 32) % warps;
+  t.padded = (warps + 3) / 4 * 4;
+  t.slots = slots + 2 * W * t.padded * (warps > 1 ? t.index : 0);
+  t.other = t.slots + W * t.padded;
+  for (int i = threadIdx.x; i < count; i += blockDim.x) slots[i] = 0.f;
+}
 
 __device__ __forceinline__ void team_sync(const Team& t) {
   if (t.warps == 1) __syncwarp();
@@ -210,19 +343,43 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Sum over the team, the same bits in every thread and on every run: lanes by
-// a butterfly, warps in their order.  The two halves of the slots alternate,
-// so that one barrier is enough: a warp that is one reduction ahead writes the
-// other half, and it cannot be two ahead.
+// a butterfly, warps in a fixed order.
 __device__ __forceinline__ float team_sum(Team& t, float x) {
   x = warp_sum(x);
   if (t.warps == 1) return x;
-  float* s = t.slots + t.turn * t.warps;
-  t.turn ^= 1;
+  float* s = t.slots;
+  t.slots = t.other;
+  t.other = s;
   if ((threadIdx.x & 31) == 0) s[t.warp] = x;
   team_sync(t);
   float r = 0.f;
-  for (int i = 0; i < t.warps; ++i) r += s[i];
+  for (int i = 0; i < t.padded; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(s + i);
+    r += (f.x + f.y) + (f.z + f.w);
+  }
   return r;
+}
+
+// Two sums at once (W = 2).  What a warp of the team wrote to shared memory
+// before it, all of them can read behind it.
+__device__ __forceinline__ void team_sum2(Team& t, float& x, float& y) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+  }
+  if (t.warps == 1) return team_sync(t);
+  float* s = t.slots;
+  t.slots = t.other;
+  t.other = s;
+  if ((threadIdx.x & 31) == 0) *reinterpret_cast<float2*>(s + 2 * t.warp) = make_float2(x, y);
+  team_sync(t);
+  x = y = 0.f;
+  for (int i = 0; i < t.padded; i += 2) {
+    const float4 f = *reinterpret_cast<const float4*>(s + 2 * i);
+    x += f.x + f.z;
+    y += f.y + f.w;
+  }
 }
 
 // Maximum of bit patterns.  Of absolute values it is the largest one, and a
@@ -230,13 +387,25 @@ __device__ __forceinline__ float team_sum(Team& t, float x) {
 __device__ __forceinline__ uint32_t team_max(Team& t, uint32_t x) {
   x = __reduce_max_sync(0xFFFFFFFFu, x);
   if (t.warps == 1) return x;
-  float* s = t.slots + t.turn * t.warps;
-  t.turn ^= 1;
+  float* s = t.slots;
+  t.slots = t.other;
+  t.other = s;
   if ((threadIdx.x & 31) == 0) s[t.warp] = __uint_as_float(x);
   team_sync(t);
   uint32_t r = 0;
-  for (int i = 0; i < t.warps; ++i) r = max(r, __float_as_uint(s[i]));
+  for (int i = 0; i < t.padded; i += 4) {
+    const uint4 f = *reinterpret_cast<const uint4*>(s + i);
+    r = max(max(r, f.x), max(f.y, max(f.z, f.w)));
+  }
   return r;
+}
+
+// x / n for n = 1 / inv: a product and a correction of its error, so that the
+// mean of equal values is that value.
+__device__ __forceinline__ float divide_by(float x, float n, float inv) {
+  const float q = x * inv;
+  const float better = fmaf(fmaf(-q, n, x), inv, q);
+  return fabsf(q) <= 3.402823466e38f ? better : q;
 }
 
 }  // namespace solattn
