@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 
 import torch
 
@@ -23,54 +24,29 @@ __all__ = ["norm_modulate", "gate_residual", "gate_residual_norm", "quantize_row
            "int8_linear", "linear_status", "AttentionLayer"]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_INT8, _FP32 = (torch.int8,), (torch.float32,)
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
 _ROPE_NORMS = {"none": 0, "head": 1, "token": 2}
 _PAIRINGS = {"interleaved": 0, "half": 1}
 _POSITIONS = {torch.int32: 1, torch.int64: 2, torch.float32: 3, torch.float64: 4}
 
-_vp, _i, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", _vp), ("dtype", _i), ("stride_b", _ll), ("stride_l", _ll)]
-
-
-class _Vectors(ctypes.Structure):
-    _fields_ = [("data", _vp), ("dtype", _i), ("groups", _i), ("stride_b", _ll), ("stride_g", _ll)]
-
-
-class _NormArgs(ctypes.Structure):
-    _fields_ = [("B", _i), ("L", _i), ("C", _i), ("x_inner", _i), ("x_stride_h", _ll), ("x", _Rows), ("y", _Rows),
-                ("x_out", _Rows), ("h", _Rows), ("q", _vp), ("q_stride", _ll), ("q_scale", _vp),
-                ("residual_scale", _f), ("norm", _i), ("eps", _f), ("post_norm", _i), ("post_eps", _f),
-                ("scale", _Vectors), ("shift", _Vectors), ("gate", _Vectors), ("weight", _Vectors),
-                ("bias", _Vectors), ("post_weight", _Vectors), ("post_bias", _Vectors)]
-
-
-class _RopeTensor(ctypes.Structure):
-    _fields_ = [("in_", _vp), ("stride_b", _ll), ("stride_l", _ll), ("stride_h", _ll), ("out", _vp),
-                ("weight", _vp), ("weight_dtype", _i)]
-
-
-class _RopeArgs(ctypes.Structure):
-    _fields_ = [("B", _i), ("L", _i), ("H", _i), ("d", _i), ("dtype", _i), ("q", _RopeTensor), ("k", _RopeTensor),
-                ("v", _RopeTensor), ("norm", _i), ("eps", _f), ("pairing", _i), ("axes", _i), ("freqs", _vp),
-                ("axis", _vp), ("pos_kind", _i), ("grid_f", _i), ("grid_h", _i), ("grid_w", _i), ("start", _ll),
-                ("positions", _vp), ("pos_stride_b", _ll), ("pos_stride_l", _ll), ("pos_stride_a", _ll)]
-
-
-class _LinearArgs(ctypes.Structure):
-    _fields_ = [("M", _i), ("N", _i), ("K", _i), ("a", _vp), ("a_stride", _ll), ("a_scale", _vp), ("w", _vp),
-                ("w_stride", _ll), ("w_scale", _vp), ("bias", _vp), ("bias_dtype", _i), ("out", _vp), ("out_dtype", _i),
-                ("out_stride", _ll)]
+# Argument structs of include/sol_attn.h, packed by struct in one call: a ctypes Structure of this many fields takes
+# longer to fill than the smallest of these operators runs.  Native alignment gives the C layout.
+_ROWS, _VECTORS, _ROPE_TENSOR = "Piqq", "Piiqq", "PqqqPPi4x"
+_NORM_ARGS = struct.Struct("@iiiiq" + 4 * _ROWS + "PqPfifif" + 7 * _VECTORS)
+_ROPE_ARGS = struct.Struct("@iiiii" + 3 * _ROPE_TENSOR + "ifiiPPiiiiqPqqq")
+_LINEAR_ARGS = struct.Struct("@iiiPqPPqPPiPiq")
+_NO_ROWS, _NO_VECTORS = (0, 0, 0, 0), (0, 0, 0, 0, 0)
+_NO_AFFINE = _NO_VECTORS + _NO_VECTORS
 
 
 # ------------------------------------------------------------------ checks
 def _input(t, name, device=None, dtypes=_DTYPES):
+    """device: the index of the device that the tensor has to be on (None: any)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has the unsupported type {t.dtype}")
     if t.requires_grad and torch.is_grad_enabled():
@@ -83,48 +59,40 @@ def _choice(value, choices, name):
     return choices[value]
 
 
-def _tokens(t, name):
-    """(B, L, C, stride_b, stride_l) of a [B, L, C] or [L, C] tensor."""
-    if t.dim() == 3:
-        B, L, C = t.shape
-        sb, sl, sc = t.stride()
-    elif t.dim() == 2:
-        (L, C), B, sb = t.shape, 1, 0
-        sl, sc = t.stride()
-    else:
-        raise ValueError(f"{name} must be [B, L, C] or [L, C]")
-    if C > 1 and sc != 1:
-        raise ValueError(f"{name}: the channels of a token must be contiguous")
-    return B, L, C, sb, sl
-
-
 def _rows(t, name):
-    _, _, _, sb, sl = _tokens(t, name)
-    return _Rows(t.data_ptr(), _DTYPES[t.dtype], sb, sl)
+    """(data, dtype, stride_b, stride_l) of a [B, L, C] or [L, C] tensor."""
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the channels of a token must be contiguous")
+    return (t.data_ptr(), _DTYPES[t.dtype], strides[0] if len(strides) == 3 else 0, strides[-2])
 
 
 def _vectors(t, name, B, L, C, device, plain=False):
     """[C], [B, C] or [B, G, C] (B may be 1: the same for every batch element); plain: [C] only."""
     if t is None:
-        return _Vectors()
+        return _NO_VECTORS
     _input(t, name, device)
-    if t.dim() == 1 and t.shape[0] == C:
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    if n == 1 and shape[0] == C:
         G, sb, sg = 1, 0, 0
-    elif t.dim() == 2 and not plain and t.shape[1] == C and t.shape[0] in (1, B):
-        G, sb, sg = 1, t.stride(0) if t.shape[0] > 1 else 0, 0
-    elif t.dim() == 3 and not plain and t.shape[2] == C and t.shape[0] in (1, B) and (t.shape[1] > 0 and L % t.shape[1] == 0):
-        G, sb, sg = t.shape[1], t.stride(0) if t.shape[0] > 1 else 0, t.stride(1)
+    elif n == 2 and not plain and shape[1] == C and shape[0] in (1, B):
+        G, sb, sg = 1, strides[0] if shape[0] > 1 else 0, 0
+    elif n == 3 and not plain and shape[2] == C and shape[0] in (1, B) and shape[1] > 0 and L % shape[1] == 0:
+        G, sb, sg = shape[1], strides[0] if shape[0] > 1 else 0, strides[1]
     else:
         want = f"[{C}]" if plain else f"[{C}], [{B}, {C}] or [{B}, G, {C}] with G dividing {L}"
-        raise ValueError(f"{name} must be {want} (got {list(t.shape)})")
-    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {want} (got {list(shape)})")
+    if C > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the channels must be contiguous")
-    return _Vectors(t.data_ptr(), _DTYPES[t.dtype], G, sb, sg)
+    return (t.data_ptr(), _DTYPES[t.dtype], G, sb, sg)
 
 
 def _output(out, name, like, dtype):
     if out is None:
-        return torch.empty(like.shape, device=like.device, dtype=dtype)
+        if like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
+        return like.new_empty(like.shape, dtype=dtype)
     if not isinstance(out, torch.Tensor) or out.device != like.device or out.dtype != dtype or out.shape != like.shape:
         raise ValueError(f"{name} must be a {dtype} tensor {list(like.shape)} on {like.device}")
     if out.requires_grad and torch.is_grad_enabled():
@@ -132,10 +100,12 @@ def _output(out, name, like, dtype):
     return out
 
 
-def _padded_rows(shape, device):
+def _padded_rows(x, shape):
     """int8 [..., K] whose rows start at multiples of 16 bytes, and its row pitch."""
-    pitch = (shape[-1] + 15) // 16 * 16
-    return torch.empty(*shape[:-1], pitch, device=device, dtype=torch.int8)[..., :shape[-1]], pitch
+    K = shape[-1]
+    pitch = (K + 15) // 16 * 16
+    t = x.new_empty((*shape[:-1], pitch), dtype=torch.int8)
+    return (t if pitch == K else t[..., :K]), pitch
 
 
 def _placed(fn):
@@ -154,71 +124,81 @@ def _placed(fn):
                             t.record_stream(stream)
                 with torch.cuda.stream(stream):
                     return fn(*args, **kw)
-            if x.device.index != torch.cuda.current_device():
+            if x.get_device() != torch.cuda.current_device():
                 with torch.cuda.device(x.device):
                     return fn(*args, **kw)
         return fn(*args, **kw)
     return call
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The handle of a device's current stream without a Stream object in between.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 # ------------------------------------------------------------------ norms
 def _norm_call(x, y, gate, scale, shift, residual_scale, post_norm, post_weight, post_bias, post_eps, norm, weight, bias,
                eps, out_dtype, quantize, x_out, want_x, want_h, out):
     _input(x, "x")
-    B, L, C, sb, sl = _tokens(x, "x")
+    shape = x.shape
+    if len(shape) == 3:
+        B, L, C = shape
+    elif len(shape) == 2:
+        B, (L, C) = 1, shape
+    else:
+        raise ValueError("x must be [B, L, C] or [L, C]")
     if C < 1:
         raise ValueError("x has no channels")
-    dev = x.device
-    a = _NormArgs(B=B, L=L, C=C, x_inner=C, x=_Rows(x.data_ptr(), _DTYPES[x.dtype], sb, sl), residual_scale=residual_scale,
-                  norm=_choice(norm, _NORMS, "norm"), eps=eps, post_norm=_choice(post_norm, _NORMS, "post_norm"),
-                  post_eps=post_eps)
+    dev, x_dtype = x.get_device(), x.dtype
+    x_rows, y_rows, xo_rows, h_rows, q_rows = _rows(x, "x"), _NO_ROWS, _NO_ROWS, _NO_ROWS, (0, 0, 0)
+    norm = _choice(norm, _NORMS, "norm")
+    post_norm = _choice(post_norm, _NORMS, "post_norm")
+    scale = _vectors(scale, "scale", B, L, C, dev)
+    shift = _vectors(shift, "shift", B, L, C, dev)
+    gates, affine, post_affine = _NO_VECTORS, _NO_AFFINE, _NO_AFFINE
     if weight is not None or bias is not None:
-        a.weight = _vectors(weight, "weight", B, L, C, dev, True)
-        a.bias = _vectors(bias, "bias", B, L, C, dev, True)
-    a.scale = _vectors(scale, "scale", B, L, C, dev)
-    a.shift = _vectors(shift, "shift", B, L, C, dev)
-    h_dtype = x.dtype
+        affine = _vectors(weight, "weight", B, L, C, dev, True) + _vectors(bias, "bias", B, L, C, dev, True)
+    h_dtype = x_dtype
     if y is not None:
         _input(y, "y", dev)
-        if y.shape != x.shape:
+        if y.shape != shape:
             raise ValueError("x and y must share one shape")
-        a.y = _rows(y, "y")
-        a.gate = _vectors(gate, "gate", B, L, C, dev)
-        if post_weight is not None or post_bias is not None:
-            a.post_weight = _vectors(post_weight, "post_weight", B, L, C, dev, True)
-            a.post_bias = _vectors(post_bias, "post_bias", B, L, C, dev, True)
         h_dtype = y.dtype
-        if y.dtype != x.dtype and x.dtype != torch.float32:
+        if h_dtype != x_dtype and x_dtype != torch.float32:
             raise ValueError("y must have the type of x, or x must be float32")
+        y_rows = _rows(y, "y")
+        gates = _vectors(gate, "gate", B, L, C, dev)
+        if post_weight is not None or post_bias is not None:
+            post_affine = (_vectors(post_weight, "post_weight", B, L, C, dev, True) +
+                           _vectors(post_bias, "post_bias", B, L, C, dev, True))
     if out_dtype is not None and out_dtype != h_dtype:
         if y is not None:
             raise ValueError("out_dtype must be the type of y")
-        if out_dtype not in _DTYPES or x.dtype != torch.float32:
+        if out_dtype not in _DTYPES or x_dtype != torch.float32:
             raise ValueError("out_dtype must be the type of x, or x must be float32")
         h_dtype = out_dtype
     if quantize and (out is not None or out_dtype is not None):
         raise ValueError("quantize=True takes neither out nor out_dtype")
-    results = []
+    results = ()
     if want_x:
-        x_out = _output(x_out, "x_out", x, x.dtype)
-        a.x_out = _rows(x_out, "x_out")
-        results.append(x_out)
+        x_out = _output(x_out, "x_out", x, x_dtype)
+        xo_rows = _rows(x_out, "x_out")
+        results = (x_out,)
     if want_h and quantize:
-        q, pitch = _padded_rows(x.shape, dev)
-        s = torch.empty(x.shape[:-1], device=dev, dtype=torch.float32)
-        a.q, a.q_stride, a.q_scale = q.data_ptr(), pitch, s.data_ptr()
-        results += [q, s]
+        q, pitch = _padded_rows(x, shape)
+        s = x.new_empty(shape[:-1], dtype=torch.float32)
+        q_rows = (q.data_ptr(), pitch, s.data_ptr())
+        results += (q, s)
     elif want_h:
         h = _output(out, "out", x, h_dtype)
-        a.h = _rows(h, "out")
-        results.append(h)
+        h_rows = _rows(h, "out")
+        results += (h,)
     if B and L:
-        _check(lib().sol_attn_norm_modulate(ctypes.byref(a), _stream(dev)))
-    return results[0] if len(results) == 1 else tuple(results)
+        args = _NORM_ARGS.pack(B, L, C, C, 0, *x_rows, *y_rows, *xo_rows, *h_rows, *q_rows, residual_scale, norm, eps,
+                               post_norm, post_eps, *scale, *shift, *gates, *affine, *post_affine)
+        rc = lib().sol_attn_norm_modulate(args, _raw_stream(dev))
+        if rc:
+            _check(rc)
+    return results[0] if len(results) == 1 else results
 
 
 @_placed
@@ -275,12 +255,15 @@ def quantize_rows(x):
         raise ValueError("x: the channels of a head must be contiguous")
     if H * d < 1:
         raise ValueError("x has no channels")
-    q, pitch = _padded_rows((B, L, H * d), x.device)
-    s = torch.empty(B, L, device=x.device, dtype=torch.float32)
-    a = _NormArgs(B=B, L=L, C=H * d, x_inner=d, x_stride_h=sh, x=_Rows(x.data_ptr(), _DTYPES[x.dtype], sb, sl),
-                  q=q.data_ptr(), q_stride=pitch, q_scale=s.data_ptr(), residual_scale=1.0)
+    q, pitch = _padded_rows(x, (B, L, H * d))
+    s = x.new_empty((B, L), dtype=torch.float32)
     if B and L:
-        _check(lib().sol_attn_norm_modulate(ctypes.byref(a), _stream(x.device)))
+        args = _NORM_ARGS.pack(B, L, H * d, d, sh, x.data_ptr(), _DTYPES[x.dtype], sb, sl, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
+                               q.data_ptr(), pitch, s.data_ptr(), 1.0, 0, 0.0, 0, 0.0, *_NO_VECTORS, *_NO_VECTORS,
+                               *_NO_VECTORS, *_NO_AFFINE, *_NO_AFFINE)
+        rc = lib().sol_attn_norm_modulate(args, _raw_stream(x.get_device()))
+        if rc:
+            _check(rc)
     return q, s
 
 
@@ -293,12 +276,37 @@ def rope_axes(d):
 
 
 @functools.lru_cache(maxsize=64)
-def _rope_pairs(axes, theta, freqs):
-    """The host arrays of a pair's frequency and axis, which depend on plain numbers only."""
+def _rope_pairs(axes, theta, freqs, d):
+    """The host arrays of a pair's frequency and axis, with their addresses; they depend on plain numbers only."""
+    if any(n < 0 or n % 2 for n in axes) or sum(axes) != d:
+        raise ValueError(f"axes must be {len(axes)} even numbers that sum to {d} (got {axes})")
     axis = [i for i, n in enumerate(axes) for _ in range(n // 2)]
     if freqs is None:
+        if not theta > 0:
+            raise ValueError("theta must be positive")
         freqs = [math.pow(theta, -2.0 * j / n) for n in axes for j in range(n // 2)]
-    return (ctypes.c_double * len(freqs))(*freqs), (ctypes.c_ubyte * len(axis))(*axis)
+    elif len(freqs) != d // 2:
+        raise ValueError(f"freqs must have {d // 2} values")
+    freq_array, axis_array = (ctypes.c_double * len(freqs))(*freqs), (ctypes.c_ubyte * len(axis))(*axis)
+    return ctypes.addressof(freq_array), ctypes.addressof(axis_array), freq_array, axis_array
+
+
+def _rope_tensor(t, name, q, w, n, out):
+    if t is not q:
+        _input(t, name, q.get_device())
+        if t.shape != q.shape or t.dtype != q.dtype:
+            raise ValueError("q, k and v must share one shape [B, L, H, d] and one type")
+    strides = t.stride()
+    if strides[3] != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    if w is None:
+        return (t.data_ptr(), *strides[:3], out.data_ptr(), 0, 0)
+    _input(w, f"{name}_weight", q.get_device())
+    if not n:
+        raise ValueError(f"{name}_weight goes with a norm")
+    if w.dim() != 1 or w.shape[0] != n or not w.is_contiguous():
+        raise ValueError(f"{name}_weight must be a contiguous [{n}]")
+    return (t.data_ptr(), *strides[:3], out.data_ptr(), w.data_ptr(), _DTYPES[w.dtype])
 
 
 @_placed
@@ -319,76 +327,51 @@ def rope(q, k, v=None, *, grid=None, positions=None, axes=None, start=0, theta=1
     if q.dim() != 4:
         raise ValueError("q, k and v must be [B, L, H, d]")
     B, L, H, d = q.shape
-    dev = q.device
+    dev = q.get_device()
     kind = _choice(norm, _ROPE_NORMS, "norm")
+    pairing = _choice(pairing, _PAIRINGS, "pairing")
     if (grid is None) == (positions is None):
         raise ValueError("give either grid or positions")
     A = 3
-    a = _RopeArgs(B=B, L=L, H=H, d=d, dtype=_DTYPES[q.dtype], norm=kind, eps=eps,
-                  pairing=_choice(pairing, _PAIRINGS, "pairing"))
     if grid is not None:
         if len(grid) != 3 or any(int(n) != n or not 1 <= n < 2 ** 31 for n in grid):
             raise ValueError(f"grid must be (frames, rows, columns), each at least 1 (got {grid!r})")
         if not 0 <= start < 2 ** 62:
             raise ValueError(f"start must not be negative (got {start!r})")
-        a.grid_f, a.grid_h, a.grid_w = (int(n) for n in grid)
-        a.start = start
+        where = (0, int(grid[0]), int(grid[1]), int(grid[2]), start, 0, 0, 0, 0)
     else:
         _input(positions, "positions", dev, _POSITIONS)
-        if positions.dim() not in (2, 3) or positions.shape[-2] != L or (positions.dim() == 3 and positions.shape[0] not in (1, B)):
-            raise ValueError(f"positions must be [{L}, A] or [{B}, {L}, A] (got {list(positions.shape)})")
+        shape, strides = positions.shape, positions.stride()
+        if len(shape) not in (2, 3) or shape[-2] != L or (len(shape) == 3 and shape[0] not in (1, B)):
+            raise ValueError(f"positions must be [{L}, A] or [{B}, {L}, A] (got {list(shape)})")
         if start:
             raise ValueError("start goes with grid")
-        A = positions.shape[-1]
-        a.pos_kind = _POSITIONS[positions.dtype]
-        a.positions = positions.data_ptr()
-        a.pos_stride_b = positions.stride(0) if positions.dim() == 3 and positions.shape[0] > 1 else 0
-        a.pos_stride_l, a.pos_stride_a = positions.stride(-2), positions.stride(-1)
+        A = shape[-1]
+        where = (_POSITIONS[positions.dtype], 0, 0, 0, 0, positions.data_ptr(),
+                 strides[0] if len(shape) == 3 and shape[0] > 1 else 0, strides[-2], strides[-1])
     if axes is None:
         if A != 3:
             raise ValueError(f"axes must be given for {A} axes")
         axes = rope_axes(d)
     axes = tuple(int(n) for n in axes)
-    if len(axes) != A or any(n < 0 or n % 2 for n in axes) or sum(axes) != d:
+    if len(axes) != A:
         raise ValueError(f"axes must be {A} even numbers that sum to {d} (got {axes})")
-    if freqs is not None:
-        freqs = tuple(float(f) for f in freqs)
-        if len(freqs) != d // 2:
-            raise ValueError(f"freqs must have {d // 2} values")
-    elif not theta > 0:
-        raise ValueError("theta must be positive")
-    freq_array, axis_array = _rope_pairs(axes, float(theta), freqs)
-    a.axes = A
-    a.freqs, a.axis = ctypes.addressof(freq_array), ctypes.addressof(axis_array)
-    outs = []
-    for name, t, w in (("q", q, q_weight), ("k", k, k_weight), ("v", v, None)):
-        if t is None and name == "v":
-            continue
-        _input(t, name, dev)
-        if t.shape != q.shape or t.dtype != q.dtype:
-            raise ValueError("q, k and v must share one shape [B, L, H, d] and one type")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}: the channels of a head must be contiguous")
-        out = torch.empty(B, H, L, d, device=dev, dtype=q.dtype)
-        outs.append(out)
-        r = _RopeTensor(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2), out.data_ptr())
-        if w is not None:
-            _input(w, f"{name}_weight", dev)
-            n = {0: 0, 1: d, 2: H * d}[kind]
-            if not n:
-                raise ValueError(f"{name}_weight goes with a norm")
-            if w.dim() != 1 or w.shape[0] != n or not w.is_contiguous():
-                raise ValueError(f"{name}_weight must be a contiguous [{n}]")
-            r.weight, r.weight_dtype = w.data_ptr(), _DTYPES[w.dtype]
-        setattr(a, name, r)
+    freq_ptr, axis_ptr, *keep = _rope_pairs(axes, float(theta), None if freqs is None else tuple(float(f) for f in freqs), d)
+    n = 0 if kind == 0 else d if kind == 1 else H * d
+    outs = [q.new_empty((B, H, L, d)) for _ in range(2 if v is None else 3)]
+    tensors = _rope_tensor(q, "q", q, q_weight, n, outs[0]) + _rope_tensor(k, "k", q, k_weight, n, outs[1])
+    tensors += (0, 0, 0, 0, 0, 0, 0) if v is None else _rope_tensor(v, "v", q, None, n, outs[2])
     if B and L and H:
-        _check(lib().sol_attn_rope(ctypes.byref(a), _stream(dev)))
+        args = _ROPE_ARGS.pack(B, L, H, d, _DTYPES[q.dtype], *tensors, kind, eps, pairing, A, freq_ptr, axis_ptr, *where)
+        rc = lib().sol_attn_rope(args, _raw_stream(dev))
+        if rc:
+            _check(rc)
     return tuple(outs)
 
 
 # ------------------------------------------------------------------ products of 8-bit integers
 def _scales(t, name, n, device):
-    _input(t, name, device, (torch.float32,))
+    _input(t, name, device, _FP32)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous values (got {list(t.shape)})")
 
@@ -401,45 +384,50 @@ def int8_linear(a, a_scale, w, w_scale, bias=None, *, out_dtype=None, out=None):
     norm_modulate(quantize=True); w: int8 [N, K] with fp32 scales [N], such as quantize_rows of a weight matrix.  The
     rows of both start at multiples of 16 bytes (as those calls return them); K is at most 131071.  bias: [N], bf16,
     fp16 or fp32.  Returns [M, N] or [B, L, N] in out_dtype (bf16, fp16 or fp32; by default bf16)."""
-    _input(a, "a", None, (torch.int8,))
-    _input(w, "w", a.device, (torch.int8,))
+    _input(a, "a", None, _INT8)
+    dev = a.get_device()
+    _input(w, "w", dev, _INT8)
     if a.dim() not in (2, 3) or w.dim() != 2 or w.shape[1] != a.shape[-1]:
         raise ValueError(f"a must be [M, K] or [B, L, K] and w [N, K] (got {list(a.shape)} and {list(w.shape)})")
     K, N = a.shape[-1], w.shape[0]
-    M = a.numel() // K if K else 0
     if K < 1:
         raise ValueError("K must be at least 1")
-    if (K > 1 and (a.stride(-1) != 1 or w.stride(1) != 1)) or \
-            (a.dim() == 3 and a.shape[0] > 1 and a.shape[1] > 1 and a.stride(0) != a.shape[1] * a.stride(1)):
+    lead, strides, w_strides = a.shape[:-1], a.stride(), w.stride()
+    M = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    if (K > 1 and (strides[-1] != 1 or w_strides[1] != 1)) or \
+            (len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and strides[0] != lead[1] * strides[1]):
         raise ValueError("the rows of a and w must be contiguous, and those of a at one pitch")
-    pitch = a.stride(-2) if a.shape[-2] > 1 else a.stride(0)
-    _scales(a_scale, "a_scale", M, a.device)
-    _scales(w_scale, "w_scale", N, a.device)
+    pitch = strides[-2] if lead[-1] > 1 else strides[0]
+    _scales(a_scale, "a_scale", M, dev)
+    _scales(w_scale, "w_scale", N, dev)
     if out is None:
         out_dtype = out_dtype or torch.bfloat16
         if out_dtype not in _DTYPES:
             raise ValueError(f"out has the unsupported type {out_dtype}")
-        out = torch.empty(*a.shape[:-1], N, device=a.device, dtype=out_dtype)
+        out = a.new_empty((*lead, N), dtype=out_dtype)
     else:
-        _input(out, "out", a.device)
-        if out.shape != (*a.shape[:-1], N) or out_dtype not in (None, out.dtype) or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous, {[*a.shape[:-1], N]} and of the type out_dtype")
-    p = _LinearArgs(M, N, K, a.data_ptr(), pitch, a_scale.data_ptr(), w.data_ptr(), w.stride(0), w_scale.data_ptr(), None, 0,
-                    out.data_ptr(), _DTYPES[out.dtype], N)
+        _input(out, "out", dev)
+        if out.shape != (*lead, N) or out_dtype not in (None, out.dtype) or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, {[*lead, N]} and of the type out_dtype")
+    b = (0, 0)
     if bias is not None:
-        _input(bias, "bias", a.device)
+        _input(bias, "bias", dev)
         if bias.shape != (N,) or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous [{N}] (got {list(bias.shape)})")
-        p.bias, p.bias_dtype = bias.data_ptr(), _DTYPES[bias.dtype]
+        b = (bias.data_ptr(), _DTYPES[bias.dtype])
     if M and N:
-        _check(lib().sol_attn_quantized_linear(ctypes.byref(p), _stream(a.device)))
+        args = _LINEAR_ARGS.pack(M, N, K, a.data_ptr(), pitch, a_scale.data_ptr(), w.data_ptr(), w_strides[0],
+                                 w_scale.data_ptr(), *b, out.data_ptr(), _DTYPES[out.dtype], N)
+        rc = lib().sol_attn_quantized_linear(args, _raw_stream(dev))
+        if rc:
+            _check(rc)
     return out
 
 
 def linear_status(device=None, stream=None):
     """Synchronises the stream and raises SolAttnError if a product on this device gave up a bounded wait."""
     with torch.cuda.device(device if stream is None else stream.device):
-        _check(lib().sol_attn_linear_status(_stream(None) if stream is None else stream.cuda_stream))
+        _check(lib().sol_attn_linear_status((torch.cuda.current_stream() if stream is None else stream).cuda_stream))
 
 
 # ------------------------------------------------------------------ the layer
@@ -479,7 +467,7 @@ class AttentionLayer:
         them; beta, chunk, flags: the attention's; grid, positions, start: rope's.  Returns (x', h') with h' in
         bf16; x_out=x updates the stream in place.  Runs on the current stream of x's device; the attention's
         workspace is the device's, so calls on one device must not overlap."""
-        _input(x, "x", self.w_qkv.device, (torch.bfloat16, torch.float32))
+        _input(x, "x", self.w_qkv.get_device(), (torch.bfloat16, torch.float32))
         if x.dim() != 3 or x.shape[2] != self.w_qkv.shape[1]:
             raise ValueError(f"x must be [B, L, {self.w_qkv.shape[1]}] (got {list(x.shape)})")
         B, L, _ = x.shape

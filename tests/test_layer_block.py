@@ -127,3 +127,28 @@ def test_refusals():
         layer(x.half(), beta=1.0, chunk=4, grid=(1, 4, 5))
     with pytest.raises(ValueError, match="grid or positions"):
         layer(x, beta=1.0, chunk=4)
+
+
+def test_packed_arguments_are_the_structs():
+    """The bindings pack their arguments in one go; the bytes are the header's structs, field by field."""
+    import ctypes
+
+    import layer_structs as st
+    from block_sparse_attention_moments_b200 import layer
+
+    def flat(cls, prefix=""):
+        for name, kind in cls._fields_:
+            if issubclass(kind, ctypes.Structure):
+                yield from flat(kind, f"{prefix}{name}.")
+            else:
+                yield f"{prefix}{name}", kind
+
+    for packer, cls in ((layer._NORM_ARGS, st.NormArgs), (layer._ROPE_ARGS, st.RopeArgs), (layer._LINEAR_ARGS, st.LinearArgs)):
+        fields = list(flat(cls))
+        assert packer.size == ctypes.sizeof(cls)
+        got = cls.from_buffer_copy(packer.pack(*range(1, len(fields) + 1)))
+        for value, (name, _) in enumerate(fields, 1):
+            x = got
+            for part in name.split("."):
+                x = getattr(x, part)
+            assert x == value, name

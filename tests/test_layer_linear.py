@@ -164,11 +164,11 @@ def test_behind_the_norm(L, C, N):
 # ------------------------------------------------------------------ refusals
 def test_entry_point_refusals():
     """The library's own checks, which come before anything is read or enqueued."""
-    from block_sparse_attention_moments_b200 import layer as ly
+    import layer_structs as ly
     lib = sa.lib()
 
     def call(**kw):
-        p = ly._LinearArgs(4, 32, 64, 0x10000, 64, 0x20000, 0x30000, 64, 0x40000, None, 0, 0x50000, 0, 32)
+        p = ly.LinearArgs(4, 32, 64, 0x10000, 64, 0x20000, 0x30000, 64, 0x40000, None, 0, 0x50000, 0, 32)
         for k, v in kw.items():
             setattr(p, k, v)
         return lib.sol_attn_quantized_linear(ly.ctypes.byref(p), None)

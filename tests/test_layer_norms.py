@@ -303,11 +303,11 @@ def test_refusals_without_a_device():
 
 def test_entry_point_refusals():
     """The library's own checks, which come before anything is read or enqueued."""
-    from block_sparse_attention_moments_b200 import layer as ly
+    import layer_structs as ly
     lib, byref = sa.lib(), ly.ctypes.byref
 
     def args(**kw):
-        a = ly._NormArgs(B=2, L=4, C=64, x_inner=64, x=ly._Rows(0x10000, 0, 256, 64), h=ly._Rows(0x90000, 0, 256, 64),
+        a = ly.NormArgs(B=2, L=4, C=64, x_inner=64, x=ly.Rows(0x10000, 0, 256, 64), h=ly.Rows(0x90000, 0, 256, 64),
                          residual_scale=1.0, norm=1, eps=1e-6)
         for k, v in kw.items():
             setattr(a, k, v)
@@ -319,22 +319,22 @@ def test_entry_point_refusals():
     assert call(B=0) == 0 and call(L=0) == 0
     assert call(norm=3) == -1 and call(post_norm=-1) == -1
     assert call(eps=-1.0) == -1 and call(eps=math.nan) == -1
-    assert call(x=ly._Rows(None, 0, 256, 64)) == -1
-    assert call(x=ly._Rows(0x10001, 0, 256, 64)) == -3
-    assert call(x=ly._Rows(0x10000, 5, 256, 64)) == -1
-    assert call(x=ly._Rows(0x10000, 0, 256, -64)) == -1
-    assert call(h=ly._Rows(0x10000, 0, 256, 64)) == -1            # h is x
-    assert call(h=ly._Rows(0x90000, 0, 256, 63)) == -1            # rows of h share elements
-    assert call(h=ly._Rows(0x90000, 2, 256, 64)) == -2            # fp32 from bf16
-    assert call(h=ly._Rows()) == -1                               # nothing to write
-    assert call(x_out=ly._Rows(0xA0000, 0, 256, 64)) == -1        # x' without y
-    assert call(y=ly._Rows(0x50000, 0, 256, 64), x_out=ly._Rows(0x50000, 0, 256, 64)) == -1
-    assert call(y=ly._Rows(0x50000, 0, 256, 64), x_out=ly._Rows(0x10080, 0, 256, 64)) == -1
-    assert call(y=ly._Rows(0x50000, 0, 256, 64), x_out=ly._Rows(0x90000, 0, 256, 64)) == -1
-    assert call(scale=ly._Vectors(0x50000, 0, 3, 64, 64)) == -1   # 3 groups of 4 tokens
-    assert call(scale=ly._Vectors(0x50000, 0, 0, 64, 64)) == -1
-    assert call(scale=ly._Vectors(0x50000, 9, 1, 64, 64)) == -1
-    assert call(scale=ly._Vectors(0x50002, 2, 1, 64, 64)) == -3
+    assert call(x=ly.Rows(None, 0, 256, 64)) == -1
+    assert call(x=ly.Rows(0x10001, 0, 256, 64)) == -3
+    assert call(x=ly.Rows(0x10000, 5, 256, 64)) == -1
+    assert call(x=ly.Rows(0x10000, 0, 256, -64)) == -1
+    assert call(h=ly.Rows(0x10000, 0, 256, 64)) == -1            # h is x
+    assert call(h=ly.Rows(0x90000, 0, 256, 63)) == -1            # rows of h share elements
+    assert call(h=ly.Rows(0x90000, 2, 256, 64)) == -2            # fp32 from bf16
+    assert call(h=ly.Rows()) == -1                               # nothing to write
+    assert call(x_out=ly.Rows(0xA0000, 0, 256, 64)) == -1        # x' without y
+    assert call(y=ly.Rows(0x50000, 0, 256, 64), x_out=ly.Rows(0x50000, 0, 256, 64)) == -1
+    assert call(y=ly.Rows(0x50000, 0, 256, 64), x_out=ly.Rows(0x10080, 0, 256, 64)) == -1
+    assert call(y=ly.Rows(0x50000, 0, 256, 64), x_out=ly.Rows(0x90000, 0, 256, 64)) == -1
+    assert call(scale=ly.Vectors(0x50000, 0, 3, 64, 64)) == -1   # 3 groups of 4 tokens
+    assert call(scale=ly.Vectors(0x50000, 0, 0, 64, 64)) == -1
+    assert call(scale=ly.Vectors(0x50000, 9, 1, 64, 64)) == -1
+    assert call(scale=ly.Vectors(0x50002, 2, 1, 64, 64)) == -3
     assert call(q=0xB0000, q_stride=64) == -1                     # no scales
     assert call(q=0xB0000, q_stride=32, q_scale=0xC0000) == -1
     assert call(x_inner=48) == -1

@@ -199,14 +199,14 @@ def test_into_the_attention():
 # ------------------------------------------------------------------ refusals
 def test_entry_point_refusals():
     """The library's own checks, which come before anything is read or enqueued."""
-    from block_sparse_attention_moments_b200 import layer as ly
+    import layer_structs as ly
     lib, c = sa.lib(), ly.ctypes
     freqs, axis = (c.c_double * 32)(*[1.0] * 32), (c.c_ubyte * 32)()
     keep = []
 
     def args(**kw):
-        t = lambda i, o: ly._RopeTensor(i, 4 * 128, 128, 64, o)
-        a = ly._RopeArgs(B=2, L=4, H=2, d=64, dtype=0, q=t(0x10000, 0x90000), k=t(0x20000, 0xA0000), axes=3,
+        t = lambda i, o: ly.RopeTensor(i, 4 * 128, 128, 64, o)
+        a = ly.RopeArgs(B=2, L=4, H=2, d=64, dtype=0, q=t(0x10000, 0x90000), k=t(0x20000, 0xA0000), axes=3,
                          freqs=c.addressof(freqs), axis=c.addressof(axis), grid_f=1, grid_h=2, grid_w=2)
         for k, v in kw.items():
             setattr(a, k, v)
@@ -222,12 +222,12 @@ def test_entry_point_refusals():
     assert call(freqs=None) == -1 and call(axis=None) == -1
     assert call(grid_f=0) == -1 and call(grid_f=1 << 16, grid_h=1 << 16) == -1 and call(start=-1) == -1
     assert call(pos_kind=5) == -1 and call(pos_kind=1) == -1 and call(pos_kind=2, positions=0x30004) == -3
-    assert call(q=ly._RopeTensor(0x10008, 512, 128, 64, 0x90000)) == -3
-    assert call(q=ly._RopeTensor(0x10000, 512, 124, 64, 0x90000)) == -3
-    assert call(q=ly._RopeTensor(0x10000, 512, -128, 64, 0x90000)) == -1
-    assert call(q=ly._RopeTensor(0x10000, 512, 128, 64, 0x10000)) == -1
-    assert call(q=ly._RopeTensor(0x10000, 512, 128, 64, 0xA0000)) == -1
-    assert call(q=ly._RopeTensor(0x10000, 512, 128, 64, 0x90000, 0x50000, 0)) == -1    # a weight without a norm
+    assert call(q=ly.RopeTensor(0x10008, 512, 128, 64, 0x90000)) == -3
+    assert call(q=ly.RopeTensor(0x10000, 512, 124, 64, 0x90000)) == -3
+    assert call(q=ly.RopeTensor(0x10000, 512, -128, 64, 0x90000)) == -1
+    assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0x10000)) == -1
+    assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0xA0000)) == -1
+    assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0x90000, 0x50000, 0)) == -1    # a weight without a norm
     bad = (c.c_double * 32)(*[math.nan] * 32)
     assert call(freqs=c.addressof(bad)) == -1
     far = (c.c_ubyte * 32)(*[3] * 32)
