@@ -281,10 +281,71 @@ int launch_linear(const LinearParams& p0, const LinearOperands& o, int dev, int 
   return SOL_ATTN_OK;
 }
 
+template <int MT, typename T>
+int launch_linear_vec(const LinearParams& p, const LinearOperands& o, int sms, cudaStream_t st) {
+  LinearVecParams v{p, o.a, o.a_pitch, o.w, o.w_pitch, 1};
+  const int groups = (p.N + kVecRows - 1) / kVecRows;
+  if (groups < kVecWarps * 8 * sms) v.split = kVecWarps;
+  const int per_block = kVecWarps / v.split;
+  linear_vec_kernel<MT, T><<<(groups + per_block - 1) / per_block, kVecWarps * 32, 0, st>>>(v);
+  CUDA_TRY(cudaGetLastError());
+  return SOL_ATTN_OK;
+}
+
+template <int BT, typename T>
+int launch_linear_few(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
+  using C = FewConfig<BT>;
+  CUtensorMap ma, mw;
+  int rc;
+  if ((rc = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.a, p.K, p.M, o.a_pitch, 128, BT))) return rc;
+  if ((rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.w, p.K, p.N, o.w_pitch, 128, 128))) return rc;
+  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
+  if (!attr_set[dev]) {
+    CUDA_TRY(cudaFuncSetAttribute(linear_few_kernel<BT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(C::kSmem)));
+    attr_set[dev] = true;
+  }
+  const int tiles = (p.N + 127) / 128, kblocks = (p.K + 127) / 128;
+  int split = 1;
+  while (split < 8 && tiles * split < sms && 2 * split <= kblocks) split *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(tiles * split);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_few_kernel<BT, T>, ma, mw, p, split));
+  return SOL_ATTN_OK;
+}
+
 template <typename T>
 int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
-  if (p.M > 128) return launch_linear<2, 256, T>(p, o, dev, sms, st);
-  return launch_linear<1, 128, T>(p, o, dev, sms, st);
+  if (p.M == 1) return launch_linear_vec<1, T>(p, o, sms, st);
+  if (p.M == 2) return launch_linear_vec<2, T>(p, o, sms, st);
+  if (p.M <= 4) return launch_linear_vec<4, T>(p, o, sms, st);
+  if (p.M <= 16) return launch_linear_few<16, T>(p, o, dev, sms, st);
+  if (p.M <= 32) return launch_linear_few<32, T>(p, o, dev, sms, st);
+  if (p.M <= 64) return launch_linear_few<64, T>(p, o, dev, sms, st);
+  if (p.M <= 128) return launch_linear_few<128, T>(p, o, dev, sms, st);
+  // The variant whose slowest SM is done first: waves of tiles, each the MMA
+  // time of its K (in units of 128 x 128 x 128 of an SM) and the time until
+  // the pipeline is full and the last output is written.
+  const auto cost = [&](int cg, int bn) {
+    const long long tiles = ((p.M + 128LL * cg - 1) / (128 * cg)) * ((p.N + bn - 1LL) / bn);
+    const long long waves = (tiles + sms / cg - 1) / (sms / cg);
+    const int kblocks = (p.K + 127) / 128;
+    const double block = cg == 2 ? 2.0 : bn == 128 ? 1.5 : 1.0;
+    return waves * (kblocks * block + bn / 64.0) + 8.0;
+  };
+  const double c2 = cost(2, 256), c1 = cost(1, 128), ch = cost(1, 64);
+  if (c2 <= c1 && c2 <= ch) return launch_linear<2, 256, T>(p, o, dev, sms, st);
+  if (c1 <= ch) return launch_linear<1, 128, T>(p, o, dev, sms, st);
+  return launch_linear<1, 64, T>(p, o, dev, sms, st);
 }
 
 }  // namespace
@@ -524,6 +585,8 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
   LinearOperands o{a->a, M > 1 ? a->a_stride : fit, a->w, N > 1 ? a->w_stride : fit};
   p.out = a->out;
   p.out_pitch = M > 1 ? a->out_stride : (N + 7LL) / 8 * 8;
+  p.vec_params = reinterpret_cast<uintptr_t>(p.w_scale) % 16 == 0 &&
+                 (!p.bias || reinterpret_cast<uintptr_t>(p.bias) % (4 * dtype_size(p.bias_dtype)) == 0);
   const Span out = span(p.out, size, 0, p.out_pitch, 1, M, N);
   if (overlap(out, span(o.a, 1, 0, o.a_pitch, 1, M, K)) || overlap(out, span(o.w, 1, 0, o.w_pitch, 1, N, K)) ||
       overlap(out, span(p.a_scale, 4, 0, 0, 1, 1, M)) || overlap(out, span(p.w_scale, 4, 0, 0, 1, 1, N)) ||

@@ -34,6 +34,7 @@ struct LinearParams {
   void* out;
   long long out_pitch;          // elements
   int direct;                   // the output's rows are not aligned for TMA
+  int vec_params;               // w_scale and bias are aligned for loads of four
 };
 
 template <int CG, int BN>
@@ -64,6 +65,8 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -131,6 +134,38 @@ __device__ __forceinline__ float bias_at(const LinearParams& p, int n) {
   float f[1][1] = {{0.f}};
   if (p.bias) load_params<1, 1>(p.bias, p.bias_dtype, n, 0, 0, 1, f);
   return f[0][0];
+}
+
+// One output value; every kernel here forms it this way, so that a token's
+// output does not depend on the number of tokens beside it.
+__device__ __forceinline__ float linear_value(int sum, float a_scale, float w_scale, float bias) {
+  return fmaf(__fmul_rn(__int2float_rn(sum), a_scale), w_scale, bias);
+}
+// Four channels of a token, with 16-byte loads of scales and bias (the same
+// addresses in all lanes).
+__device__ __forceinline__ void linear_values4(const LinearParams& p, const uint32_t* sum, float a_scale, int n, float* f) {
+  const float4 w = *reinterpret_cast<const float4*>(p.w_scale + n);
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.bias) {
+    if (p.bias_dtype == kDtypeFp32) {
+      b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + n);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + n);
+      if (p.bias_dtype == kDtypeBf16) {
+        widen2<__nv_bfloat16>(u.x, b.x, b.y);
+        widen2<__nv_bfloat16>(u.y, b.z, b.w);
+      } else {
+        widen2<__half>(u.x, b.x, b.y);
+        widen2<__half>(u.y, b.z, b.w);
+      }
+    }
+  }
+  const float2 s = make_float2(a_scale, a_scale);
+  const float2 x = __fmul2_rn(make_float2(__int2float_rn(sum[0]), __int2float_rn(sum[1])), s);
+  const float2 y = __fmul2_rn(make_float2(__int2float_rn(sum[2]), __int2float_rn(sum[3])), s);
+  const float2 u = __ffma2_rn(x, make_float2(w.x, w.y), make_float2(b.x, b.y));
+  const float2 v = __ffma2_rn(y, make_float2(w.z, w.w), make_float2(b.z, b.w));
+  f[0] = u.x, f[1] = u.y, f[2] = v.x, f[3] = v.y;
 }
 
 __device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int* m, int* n) {
@@ -261,13 +296,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         }
         __syncwarp();
+        const bool fast = p.vec_params && col0 + kCols <= p.N;
 #pragma unroll
         for (int j = 0; j < kCols; j += 16 / sizeof(T)) {
           float f[16 / sizeof(T)];
+          if (fast) {
 #pragma unroll
-          for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) {
-            const int n = min(col0 + j + i, p.N - 1);
-            f[i] = fmaf(static_cast<float>(static_cast<int>(r[j + i])) * sa, p.w_scale[n], bias_at(p, n));
+            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); i += 4) linear_values4(p, r + j + i, sa, col0 + j + i, f + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) {
+              const int n = min(col0 + j + i, p.N - 1);
+              f[i] = linear_value(r[j + i], sa, p.w_scale[n], bias_at(p, n));
+            }
           }
           uint4 w;
           if constexpr (sizeof(T) == 2)
@@ -287,12 +328,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         } else {
           __syncwarp();
           const int rows = min(32, p.M - row0), cols = min(kCols, p.N - col0);
-          for (int i = 0; i < rows; ++i) {
-            T* o = static_cast<T*>(p.out) + (row0 + i) * p.out_pitch + col0;
-            for (int j = lane; j < cols; j += 32) {
-              const int byte = j * static_cast<int>(sizeof(T));
-              o[j] = *reinterpret_cast<const T*>(sbuf + i * 128 + (((byte >> 4) ^ (i & 7)) << 4) + (byte & 15));
-            }
+          T* o = static_cast<T*>(p.out) + row0 * p.out_pitch + col0;
+#pragma unroll
+          for (int j0 = 0; j0 < kCols; j0 += 32) {
+            const int byte = (j0 + lane) * static_cast<int>(sizeof(T));
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i)
+              if (i < rows && j0 + lane < cols)
+                o[i * p.out_pitch + j0 + lane] =
+                    *reinterpret_cast<const T*>(sbuf + i * 128 + (((byte >> 4) ^ (i & 7)) << 4) + (byte & 15));
           }
           __syncwarp();
         }
@@ -313,6 +357,235 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   else __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_all<CG>(tmem, C::kTmem);
+}
+
+
+// ------------------------------------------------------------------ one to four tokens
+// The weights are read once and each of their bytes meets MT tokens: bound by
+// their bytes, so plain 16-byte loads and dp4a.  A warp takes R channels, its
+// lanes 16 bytes each of K a step; where there are few channels the block's
+// warps share them and split K.
+constexpr int kVecRows = 4;      // channels of a warp
+constexpr int kVecWarps = 4;     // warps of a block
+
+struct LinearVecParams {
+  LinearParams p;
+  const int8_t* a;
+  long long a_pitch;
+  const int8_t* w;
+  long long w_pitch;
+  int split;      // warps that share channels: 1 or kVecWarps
+};
+
+// 16 bytes of a row of K bytes at k; bytes past the row read as zero.
+__device__ __forceinline__ int4 load_row16(const int8_t* row, int k, int K) {
+  if (k + 16 <= K) {
+    int4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(row + k));
+    return r;
+  }
+  int v[4] = {0, 0, 0, 0};
+  for (int i = 0; k + i < K; ++i) v[i / 4] |= (row[k + i] & 255) << (8 * (i % 4));
+  return make_int4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ int dot16(const int4& a, const int4& b, int s) {
+  return __dp4a(a.w, b.w, __dp4a(a.z, b.z, __dp4a(a.y, b.y, __dp4a(a.x, b.x, s))));
+}
+
+template <int MT, typename T>
+__global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid_constant__ LinearVecParams v) {
+  __shared__ int part[kVecWarps][kVecRows * MT];
+  const LinearParams& p = v.p;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int sub = warp % v.split;   // this warp's share of K
+  const int n0 = (blockIdx.x * (kVecWarps / v.split) + warp / v.split) * kVecRows;
+  int acc[kVecRows][MT];
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+  const int8_t* w[kVecRows];
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r) w[r] = v.w + static_cast<long long>(min(n0 + r, p.N - 1)) * v.w_pitch;
+  constexpr int U = MT <= 2 ? 2 : 1;   // steps under way together
+  for (int k = (sub * 32 + lane) * 16; k < p.K; k += U * v.split * 512) {
+    int4 x[U][kVecRows], y[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ku = k + u * v.split * 512;
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r) x[u][r] = ku < p.K ? load_row16(w[r], ku, p.K) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        y[u][m] = ku < p.K && m < p.M ? (ku + 16 <= p.K ? *reinterpret_cast<const int4*>(v.a + m * v.a_pitch + ku)
+                                                        : load_row16(v.a + m * v.a_pitch, ku, p.K))
+                                      : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = dot16(x[u][r], y[u][m], acc[r][m]);
+  }
+  int mine = 0;   // the sum of channel lane / MT and token lane % MT
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int s = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
+      if (lane == r * MT + m) mine = s;
+    }
+  if (v.split > 1) {
+    if (lane < kVecRows * MT) part[warp][lane] = mine;
+    __syncthreads();
+    if (sub) return;
+    if (lane < kVecRows * MT)
+      for (int i = 1; i < v.split; ++i) mine += part[warp + i][lane];
+  }
+  const int n = n0 + lane / MT, m = lane % MT;
+  if (lane < kVecRows * MT && n < p.N && m < p.M)
+    static_cast<T*>(p.out)[m * p.out_pitch + n] = from_f32<T>(linear_value(mine, p.a_scale[m], p.w_scale[n], bias_at(p, n)));
+}
+
+// ------------------------------------------------------------------ up to 128 tokens
+// The tile the other way round: 128 channels are the rows of the MMA and BT
+// tokens its columns, so that the weights, which bound it, fill whole tiles.
+// A cluster of `split` CTAs shares a tile's K; each reads its accumulators and
+// gives every rank the sums of that rank's tokens through distributed shared
+// memory, where the rank adds them in order.  One tile to a cluster, a few
+// CTAs to an SM.
+template <int BT>
+struct FewConfig {
+  static constexpr int kStage = kLinStageA + BT * 128;
+  static constexpr int kStages = BT <= 32 ? 4 : BT == 64 ? 3 : 3;
+  static constexpr int kParts = BT * 128 * 4;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kParts + 1024 + 256;
+};
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+template <int BT, typename T>
+__global__ void __launch_bounds__(kLinThreads)
+    linear_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ LinearParams p, int split) {
+  using C = FewConfig<BT>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint32_t* parts = reinterpret_cast<uint32_t*>(base + C::kStages * C::kStage);   // [split][BT / split][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(parts + BT * 128);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr int kTmem = BT < 32 ? 32 : BT;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int n0 = (blockIdx.x / split) * 128;
+  if (split > 1) cluster_arrive();   // met before the first access to another CTA's memory, which must have started
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_all<1>(tmem_slot, kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int kblocks = (p.K + 127) / 128;
+  const int k0 = kblocks * rank / split, k1 = kblocks * (rank + 1) / split;   // never empty: split <= kblocks
+  bool ok = true;
+  if (warp == 0 && lane == 0) {
+    for (int k = k0; k < k1; ++k) {
+      const int it = k - k0, s = it % C::kStages;
+      if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort, kLinTimeoutNs)) { ok = false; break; }
+      mbar_arrive_expect_tx(&full[s], C::kStage);
+      const uint32_t dst = smem_u32(base + s * C::kStage);
+      tma_load_2d<1>(dst, &map_w, smem_u32(&full[s]), k * 128, n0);
+      tma_load_2d<1>(dst + kLinStageA, &map_a, smem_u32(&full[s]), k * 128, 0);
+    }
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = idesc_s8_s32(128, BT);
+    for (int k = k0; k < k1; ++k) {
+      const int it = k - k0, s = it % C::kStages;
+      if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort, kLinTimeoutNs)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t sw = smem_u32(base + s * C::kStage);
+      const uint64_t dw = sdesc_sw128(sw, 16, 1024), da = sdesc_sw128(sw + kLinStageA, 16, 1024);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_s8<1>(tmem, dw + 2 * j, da + 2 * j, idesc, (it | j) != 0);
+      umma_commit(&empty[s]);
+    }
+    if (ok) umma_commit(acc_full);
+  }
+  const int q = warp & 3, row = q * 32 + lane;   // of warps 2 to 5: this thread's channel of the tile
+  uint32_t r[BT];
+  if (warp >= 2) {
+    ok = mbar_wait(acc_full, 0, abort, kLinTimeoutNs);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    tc_fence_after();
+    if (ok) {
+      const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      if constexpr (BT < 32) {
+        tmem_ld_x16f(src, reinterpret_cast<float*>(r));
+      } else {
+#pragma unroll
+        for (int j = 0; j < BT; j += 32) tmem_ld_x32f(src + j, reinterpret_cast<float*>(r) + j);
+      }
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < BT; j += 16) reg_fence16(reinterpret_cast<float*>(r) + j);
+    }
+  }
+  if (!ok) {
+    *abort = 1;
+    atomicOr(&g_linear_status, 1u);
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {}
+  }
+  __syncwarp();
+  const int n = n0 + row;
+  if (split > 1) {
+    const int each = BT / split;   // tokens of a rank
+    cluster_wait();
+    if (warp >= 2) {
+      const uint32_t mine = smem_u32(parts + (rank * each) * 128 + row);
+#pragma unroll
+      for (int j = 0; j < BT; ++j)
+        st_cluster(map_to_rank(mine + (j % each) * 512, j / each), r[j]);
+    }
+    cluster_sync();
+    if (warp >= 2 && n < p.N) {
+      const float ws = p.w_scale[n], b = bias_at(p, n);
+      for (int j = 0; j < each; ++j) {
+        const int m = rank * each + j;
+        if (m >= p.M) break;
+        int sum = 0;
+        for (int s = 0; s < split; ++s) sum += parts[(s * each + j) * 128 + row];
+        static_cast<T*>(p.out)[m * p.out_pitch + n] = from_f32<T>(linear_value(sum, p.a_scale[m], ws, b));
+      }
+    }
+  } else if (warp >= 2 && n < p.N) {
+    const float ws = p.w_scale[n], b = bias_at(p, n);
+#pragma unroll
+    for (int j = 0; j < BT; ++j)
+      if (j < p.M) static_cast<T*>(p.out)[j * p.out_pitch + n] = from_f32<T>(linear_value(r[j], p.a_scale[j], ws, b));
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_all<1>(tmem, kTmem);
 }
 
 }  // namespace solattn
