@@ -306,8 +306,9 @@ int launch_linear_few(const LinearParams& p, const LinearOperands& o, int dev, i
     attr_set[dev] = true;
   }
   const int tiles = (p.N + 127) / 128, kblocks = (p.K + 127) / 128;
-  int split = 1;
-  while (split < 8 && tiles * split < sms && 2 * split <= kblocks) split *= 2;
+  int log_split = 0;
+  while (log_split < 3 && (tiles << log_split) < sms && (2 << log_split) <= kblocks) ++log_split;
+  const int split = 1 << log_split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * split);
   cfg.blockDim = dim3(kLinThreads);
@@ -319,7 +320,7 @@ int launch_linear_few(const LinearParams& p, const LinearOperands& o, int dev, i
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_few_kernel<BT, T>, ma, mw, p, split));
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_few_kernel<BT, T>, ma, mw, p, log_split));
   return SOL_ATTN_OK;
 }
 
@@ -585,8 +586,6 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
   LinearOperands o{a->a, M > 1 ? a->a_stride : fit, a->w, N > 1 ? a->w_stride : fit};
   p.out = a->out;
   p.out_pitch = M > 1 ? a->out_stride : (N + 7LL) / 8 * 8;
-  p.vec_params = reinterpret_cast<uintptr_t>(p.w_scale) % 16 == 0 &&
-                 (!p.bias || reinterpret_cast<uintptr_t>(p.bias) % (4 * dtype_size(p.bias_dtype)) == 0);
   const Span out = span(p.out, size, 0, p.out_pitch, 1, M, N);
   if (overlap(out, span(o.a, 1, 0, o.a_pitch, 1, M, K)) || overlap(out, span(o.w, 1, 0, o.w_pitch, 1, N, K)) ||
       overlap(out, span(p.a_scale, 4, 0, 0, 1, 1, M)) || overlap(out, span(p.w_scale, 4, 0, 0, 1, 1, N)) ||

@@ -34,7 +34,6 @@ struct LinearParams {
   void* out;
   long long out_pitch;          // elements
   int direct;                   // the output's rows are not aligned for TMA
-  int vec_params;               // w_scale and bias are aligned for loads of four
 };
 
 template <int CG, int BN>
@@ -44,7 +43,9 @@ struct LinearConfig {
   static constexpr int kOut = 4 * 2 * 4096;              // per epilogue warp two buffers of 32 rows x 128 bytes
   static constexpr int kStages = (224 * 1024 - kOut) / kStage > 8 ? 8 : (224 * 1024 - kOut) / kStage;
   static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kOut + 1024 + 512;
+  static constexpr int kParams = BN * 8;                 // the tile's scales and biases, fp32
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kOut + kParams + 512;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
 
 // kind::i8 instruction descriptor: D s32 (2), A and B s8 (1), both K-major.
@@ -141,25 +142,8 @@ __device__ __forceinline__ float bias_at(const LinearParams& p, int n) {
 __device__ __forceinline__ float linear_value(int sum, float a_scale, float w_scale, float bias) {
   return fmaf(__fmul_rn(__int2float_rn(sum), a_scale), w_scale, bias);
 }
-// Four channels of a token, with 16-byte loads of scales and bias (the same
-// addresses in all lanes).
-__device__ __forceinline__ void linear_values4(const LinearParams& p, const uint32_t* sum, float a_scale, int n, float* f) {
-  const float4 w = *reinterpret_cast<const float4*>(p.w_scale + n);
-  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.bias) {
-    if (p.bias_dtype == kDtypeFp32) {
-      b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + n);
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + n);
-      if (p.bias_dtype == kDtypeBf16) {
-        widen2<__nv_bfloat16>(u.x, b.x, b.y);
-        widen2<__nv_bfloat16>(u.y, b.z, b.w);
-      } else {
-        widen2<__half>(u.x, b.x, b.y);
-        widen2<__half>(u.y, b.z, b.w);
-      }
-    }
-  }
+// The same for four channels of a token.
+__device__ __forceinline__ void linear_values4(const uint32_t* sum, float a_scale, const float4& w, const float4& b, float* f) {
   const float2 s = make_float2(a_scale, a_scale);
   const float2 x = __fmul2_rn(make_float2(__int2float_rn(sum[0]), __int2float_rn(sum[1])), s);
   const float2 y = __fmul2_rn(make_float2(__int2float_rn(sum[2]), __int2float_rn(sum[3])), s);
@@ -176,15 +160,25 @@ __device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int* m
   *m = b * p.band + (r - *n * rows);
 }
 
+// Barrier 1 of the four epilogue warps; whether all of their threads are well.
+__device__ __forceinline__ bool all_of_epilogue(bool ok) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(ok))
+               : "memory");
+  return r != 0;
+}
+
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
   using C = LinearConfig<CG, BN>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* out_buf = base + C::kStages * C::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_buf + C::kOut);
+  float* params = reinterpret_cast<float*>(out_buf + C::kOut);   // scales, then biases, of the tile's channels
+  uint64_t* full = reinterpret_cast<uint64_t*>(params + 2 * BN);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -261,15 +255,35 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint8_t* stage_out = out_buf + q * 2 * 4096;
     constexpr int kCols = 128 / sizeof(T);  // channels of a 128-byte row of the output buffer
     int tile = 0, chunk = 0;
-    for (int t = first; t < tiles && ok; t += step, ++tile) {
+    for (int t = first; t < tiles; t += step, ++tile) {
       int tm, tn;
       linear_tile(p, t, &tm, &tn);
       const int buf = tile & 1;
       const int row0 = (tm * CG + static_cast<int>(rank)) * 128 + q * 32;
       const int row = row0 + lane;
       const float sa = row < p.M ? p.a_scale[row] : 0.f;
+      // the channels' scales and biases, fetched while the tile is being multiplied
+      float mine[2][BN / 128 > 0 ? BN / 128 : 1];
+#pragma unroll
+      for (int i = 0; i < (BN + 127) / 128; ++i) {
+        const int n = tn * BN + i * 128 + q * 32 + lane;
+        const bool there = i * 128 + q * 32 + lane < BN && n < p.N;
+        mine[0][i] = there ? p.w_scale[n] : 0.f;
+        mine[1][i] = there ? bias_at(p, n) : 0.f;
+      }
+      // Those of the tile before have been read.  A warp whose wait gave up
+      // says so here, where the four leave together: none is left at a barrier.
+      ok = all_of_epilogue(ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < (BN + 127) / 128; ++i) {
+        const int c = i * 128 + q * 32 + lane;
+        if (c < BN) params[c] = mine[0][i], params[BN + c] = mine[1][i];
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
       ok = mbar_wait(&acc_full[buf], (tile >> 1) & 1, abort, kLinTimeoutNs);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
       for (int c0 = 0; c0 < BN; c0 += kCols) {
@@ -296,20 +310,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         }
         __syncwarp();
-        const bool fast = p.vec_params && col0 + kCols <= p.N;
 #pragma unroll
         for (int j = 0; j < kCols; j += 16 / sizeof(T)) {
           float f[16 / sizeof(T)];
-          if (fast) {
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); i += 4) linear_values4(p, r + j + i, sa, col0 + j + i, f + i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) {
-              const int n = min(col0 + j + i, p.N - 1);
-              f[i] = linear_value(r[j + i], sa, p.w_scale[n], bias_at(p, n));
-            }
-          }
+          for (int i = 0; i < static_cast<int>(16 / sizeof(T)); i += 4)
+            linear_values4(r + j + i, sa, *reinterpret_cast<const float4*>(params + c0 + j + i),
+                           *reinterpret_cast<const float4*>(params + BN + c0 + j + i), f + i);
           uint4 w;
           if constexpr (sizeof(T) == 2)
             w = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]), narrow2<T>(f[6], f[7]));
@@ -462,7 +469,7 @@ struct FewConfig {
   static constexpr int kStage = kLinStageA + BT * 128;
   static constexpr int kStages = BT <= 32 ? 4 : BT == 64 ? 3 : 3;
   static constexpr int kParts = BT * 128 * 4;
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kParts + 1024 + 256;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kParts + BT * 4 + 256;
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
@@ -472,12 +479,12 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
 template <int BT, typename T>
 __global__ void __launch_bounds__(kLinThreads)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                      const __grid_constant__ LinearParams p, int split) {
+                      const __grid_constant__ LinearParams p, int log_split) {
   using C = FewConfig<BT>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];
   uint32_t* parts = reinterpret_cast<uint32_t*>(base + C::kStages * C::kStage);   // [split][BT / split][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(parts + BT * 128);
+  float* a_scale = reinterpret_cast<float*>(parts + BT * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(a_scale + BT);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kLinThreads)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
-  const int n0 = (blockIdx.x / split) * 128;
+  const int split = 1 << log_split, n0 = (blockIdx.x >> log_split) * 128;
   if (split > 1) cluster_arrive();   // met before the first access to another CTA's memory, which must have started
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -498,6 +505,7 @@ __global__ void __launch_bounds__(kLinThreads)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_all<1>(tmem_slot, kTmem);
+  for (int i = threadIdx.x; i < BT; i += kLinThreads) a_scale[i] = i < p.M ? p.a_scale[i] : 0.f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -529,6 +537,8 @@ __global__ void __launch_bounds__(kLinThreads)
     if (ok) umma_commit(acc_full);
   }
   const int q = warp & 3, row = q * 32 + lane;   // of warps 2 to 5: this thread's channel of the tile
+  const int n = n0 + row;
+  const float ws = warp >= 2 && n < p.N ? p.w_scale[n] : 0.f, b = warp >= 2 && n < p.N ? bias_at(p, n) : 0.f;
   uint32_t r[BT];
   if (warp >= 2) {
     ok = mbar_wait(acc_full, 0, abort, kLinTimeoutNs);
@@ -554,32 +564,31 @@ __global__ void __launch_bounds__(kLinThreads)
     while (globaltimer_ns() - t0 < 2000000ull) {}
   }
   __syncwarp();
-  const int n = n0 + row;
   if (split > 1) {
-    const int each = BT / split;   // tokens of a rank
+    const int each = BT >> log_split;   // tokens of a rank
     cluster_wait();
     if (warp >= 2) {
       const uint32_t mine = smem_u32(parts + (rank * each) * 128 + row);
 #pragma unroll
-      for (int j = 0; j < BT; ++j)
-        st_cluster(map_to_rank(mine + (j % each) * 512, j / each), r[j]);
+      for (int j = 0; j < BT; ++j)   // each is a power of two
+        st_cluster(map_to_rank(mine + (j & (each - 1)) * 512, j >> (31 - __clz(each))), r[j]);
     }
     cluster_sync();
     if (warp >= 2 && n < p.N) {
-      const float ws = p.w_scale[n], b = bias_at(p, n);
-      for (int j = 0; j < each; ++j) {
-        const int m = rank * each + j;
-        if (m >= p.M) break;
+      const int m0 = rank * each, count = min(each, p.M - m0);
+      T* o = static_cast<T*>(p.out) + m0 * p.out_pitch + n;
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) {
         int sum = 0;
         for (int s = 0; s < split; ++s) sum += parts[(s * each + j) * 128 + row];
-        static_cast<T*>(p.out)[m * p.out_pitch + n] = from_f32<T>(linear_value(sum, p.a_scale[m], ws, b));
+        o[j * p.out_pitch] = from_f32<T>(linear_value(sum, a_scale[m0 + j], ws, b));
       }
     }
   } else if (warp >= 2 && n < p.N) {
-    const float ws = p.w_scale[n], b = bias_at(p, n);
+    T* o = static_cast<T*>(p.out) + n;
 #pragma unroll
     for (int j = 0; j < BT; ++j)
-      if (j < p.M) static_cast<T*>(p.out)[j * p.out_pitch + n] = from_f32<T>(linear_value(r[j], p.a_scale[j], ws, b));
+      if (j < p.M) o[j * p.out_pitch] = from_f32<T>(linear_value(r[j], a_scale[j], ws, b));
   }
   __syncwarp();
   tc_fence_before();
