@@ -21,7 +21,12 @@ namespace {
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
 constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
-constexpr int kNormRingRows = 32;                // rows of a block, and of a group, from which it is taken
+constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
+constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
+// Rows of a team at a time: two share the factors' reads and the barriers; of
+// an fp32 stream and a block's output two do not leave room for enough teams.
+template <typename TX, bool RES>
+constexpr int kNormRingRows = RES && sizeof(TX) == 4 ? 1 : 2;
 constexpr size_t kRopeShared = 220 * 1024;       // shared memory of the rotary kernel
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
@@ -127,40 +132,54 @@ int launch_norm_as(NormParams p, int sms, cudaStream_t st) {
 }
 
 // Whether the call is one for the ring kernel; if it is, *rc is its status.
-template <typename TX, typename TY, bool RES, bool FULL>
-bool launch_norm_ring(NormParams p, int dev, int sms, cudaStream_t st, int* rc) {
-  constexpr int N = 4, THREADS = RES ? 640 : 800;
-  const long long rows = static_cast<long long>(p.B) * p.L;
-  const int per_warp = 32 * N * 8;
-  p.warps = (p.C + per_warp - 1) / per_warp;
-  if (FULL && p.C % per_warp) return launch_norm_ring<TX, TY, RES, false>(p, dev, sms, st, rc);
-  if (rows < kNormRingRows * static_cast<long long>(sms) || p.group < kNormRingRows || p.warps * 32 > THREADS) return false;
-  const int teams = p.warps > 1 ? std::min(15, THREADS / 32 / p.warps) : THREADS / 32;
-  const size_t factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
-  const size_t stage = static_cast<size_t>(teams) * p.warps * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-  if (factors + stage > kNormRingShared) return false;
-  p.depth = static_cast<int>(std::min<size_t>(4, (kNormRingShared - factors) / stage));
+template <typename TX, typename TY, bool RES, bool FULL, int WARPS>
+int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_t st) {
+  constexpr int R = kNormRingRows<TX, RES>, N = kNormRingVectors;
+  const int teams = p.warps > 1 ? std::min(15, kNormRingThreads / 32 / p.warps) : kNormRingThreads / 32;
+  const size_t row = static_cast<size_t>(p.warps) * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
+  const int fit = static_cast<int>((kNormRingShared - factors) / (R * row));   // stages of all teams
+  const int used = std::min(teams, fit);
+  p.depth = std::min(4, fit / used);
   static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_ring_kernel<TX, TY, N, RES, FULL, THREADS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormRingShared));
-    if (e != cudaSuccess) {
-      *rc = fail(SOL_ATTN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-      return true;
-    }
+    CUDA_TRY(cudaFuncSetAttribute(norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormRingShared)));
     attr_set[dev] = true;
   }
-  norm_ring_kernel<TX, TY, N, RES, FULL, THREADS><<<sms, teams * p.warps * 32, factors + p.depth * stage, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  *rc = e == cudaSuccess ? SOL_ATTN_OK : fail(SOL_ATTN_ERR_CUDA, "norm kernel: %s", cudaGetErrorString(e));
-  return true;
+  norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>
+      <<<sms, used * p.warps * 32, factors + static_cast<size_t>(used) * p.depth * R * row, st>>>(p);
+  CUDA_TRY(cudaGetLastError());
+  return SOL_ATTN_OK;
+}
+
+// Whether the ring kernel takes the call: many rows of long groups, vectors of
+// 8, and factors that leave room for two teams' rows.
+template <typename TX, typename TY, bool RES>
+bool for_norm_ring(NormParams& p, size_t* factors, int sms) {
+  const long long rows = static_cast<long long>(p.B) * p.L;
+  const int per_warp = 32 * kNormRingVectors * 8;
+  p.warps = (p.C + per_warp - 1) / per_warp;
+  *factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
+  const size_t row = static_cast<size_t>(p.warps) * kNormRingVectors * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
+  for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
+  return rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
+         (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift) &&
+         *factors + 2 * kNormRingRows<TX, RES> * row <= kNormRingShared;
 }
 
 template <typename TX, typename TY, bool RES>
 int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
-  int rc;
   if (vec) {
-    if (launch_norm_ring<TX, TY, RES, true>(p, dev, sms, st, &rc)) return rc;
+    NormParams r = p;
+    size_t factors;
+    if (for_norm_ring<TX, TY, RES>(r, &factors, sms)) {
+      const bool full = p.C % (32 * kNormRingVectors * 8) == 0;
+      if (r.warps == 1)
+        return full ? launch_norm_ring<TX, TY, RES, true, 1>(r, factors, dev, sms, st)
+                    : launch_norm_ring<TX, TY, RES, false, 1>(r, factors, dev, sms, st);
+      return full ? launch_norm_ring<TX, TY, RES, true, 8>(r, factors, dev, sms, st)
+                  : launch_norm_ring<TX, TY, RES, false, 8>(r, factors, dev, sms, st);
+    }
     if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
     return launch_norm_as<TX, TY, 8, 4, RES, 512>(p, sms, st);
   }
@@ -174,11 +193,9 @@ int launch_norm_res(const NormParams& p, bool vec, int dev, int sms, cudaStream_
   return p.y ? launch_norm<TX, TY, true>(p, vec, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, dev, sms, st);
 }
 
-template <typename T, bool HALF>
+template <typename T, bool HALF, int WARPS>
 int launch_rope_as(RopeParams p, int dev, int sms, cudaStream_t st) {
-  constexpr int N = kRopeVectors / (HALF ? 2 : 1);
   const int items = p.H * p.d / (HALF ? 16 : 8);
-  p.warps = (items + 32 * N - 1) / (32 * N);
   const int group = p.d / (HALF ? 16 : 8);
   p.by_lanes = 32 % group == 0;
   // per team and parity: cosines and sines, and the items' sums where lanes cannot add them
@@ -197,20 +214,29 @@ int launch_rope_as(RopeParams p, int dev, int sms, cudaStream_t st) {
   const size_t smem = weights + teams * (2 * p.team_floats * sizeof(float) + p.depth * stage);
   static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
   if (!attr_set[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(rope_kernel<T, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    CUDA_TRY(cudaFuncSetAttribute(rope_kernel<T, HALF, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   static_cast<int>(kRopeShared)));
     attr_set[dev] = true;
   }
   const long long tokens = static_cast<long long>(p.B) * p.L;
   const int grid = static_cast<int>(std::min<long long>((tokens + teams - 1) / teams, sms));
-  rope_kernel<T, HALF><<<grid, teams * p.warps * 32, smem, st>>>(p);
+  rope_kernel<T, HALF, WARPS><<<grid, teams * p.warps * 32, smem, st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
 }
 
+template <typename T, bool HALF>
+int launch_rope_warps(RopeParams p, int dev, int sms, cudaStream_t st) {
+  const int per_warp = 32 * kRopeVectors * 8;
+  p.warps = (p.H * p.d + per_warp - 1) / per_warp;
+  if (p.warps == 1) return launch_rope_as<T, HALF, 1>(p, dev, sms, st);
+  if (p.warps <= 8) return launch_rope_as<T, HALF, 8>(p, dev, sms, st);
+  return launch_rope_as<T, HALF, 16>(p, dev, sms, st);
+}
+
 template <typename T>
 int launch_rope(const RopeParams& p, int dev, int sms, cudaStream_t st) {
-  return p.half ? launch_rope_as<T, true>(p, dev, sms, st) : launch_rope_as<T, false>(p, dev, sms, st);
+  return p.half ? launch_rope_warps<T, true>(p, dev, sms, st) : launch_rope_warps<T, false>(p, dev, sms, st);
 }
 
 // 2-D map of rows of K elements (pitch in bytes) with a {box_k, box_rows} box

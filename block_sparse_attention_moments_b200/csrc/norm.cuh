@@ -24,6 +24,8 @@
 
 namespace solattn {
 
+constexpr int kNormRingThreads = 512;
+
 enum : int { kNormNone = 0, kNormLayer = 1, kNormRms = 2 };
 
 // [B, G, C]: group g covers `per` consecutive tokens.  p is null where absent.
@@ -57,6 +59,7 @@ struct NormParams {
   int group;                      // tokens that share all of their vectors
   int depth;                      // stages of the ring
   float channels, inv_channels;   // C and 1 / C
+  int inner_shift;                // log2 of x_inner, where the ring kernel reads pieces
 };
 
 // The folded factors of N vectors of V channels, c, c + step, ...
@@ -130,104 +133,136 @@ __device__ __forceinline__ void get_factor(const float* plane, int nvec, int vec
   }
 }
 
-// Normalises a row that the team holds in registers (no weight or bias).
-template <int V, int N>
-__device__ __forceinline__ void normalise(Team& t, int kind, float eps, const NormParams& p, const bool (&on)[N], float (&v)[N][V]) {
+// Normalises R rows that the team holds in registers (no weight or bias).
+template <int R, int V, int N, class Team>
+__device__ __forceinline__ void normalise(Team& t, int kind, float eps, const NormParams& p, const bool (&on)[N],
+                                          float (&v)[R][N][V]) {
   if (kind == kNormNone) return;
+  float x[R];
   if (kind == kNormLayer) {
-    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum_v<V>(s, v[i]);   // zero outside the row
-    const float mean = divide_by(team_sum(t, s.x + s.y), p.channels, p.inv_channels);
+    for (int r = 0; r < R; ++r) {
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (on[i]) add_s<V>(v[i], -mean);
-  }
-  float2 s = make_float2(0.f, 0.f);
+      for (int i = 0; i < N; ++i) sum_v<V>(s, v[r][i]);   // zero outside the row
+      x[r] = s.x + s.y;
+    }
+    t.template sum<R>(x);
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum_sq<V>(s, v[i]);
-  const float r = rsqrtf(fmaf(team_sum(t, s.x + s.y), p.inv_channels, eps));
-#pragma unroll
-  for (int i = 0; i < N; ++i) mul_s<V>(v[i], r);
-}
-
-// What happens to a row v = x' (unrounded) of a team: x' is written, normed,
-// modulated with the factors that pre(i, a, c) gives, and written as h and in
-// 8 bits.
-template <typename TX, typename TY, int V, int N, bool RES, class Pre>
-__device__ __forceinline__ void emit_row(const NormParams& p, Team& team, unsigned row, int b, int l, int first,
-                                         const bool (&on)[N], float (&v)[N][V], Pre pre) {
-  if constexpr (RES) {
-    if (p.xo) {
-      TX* op = static_cast<TX*>(p.xo) + b * p.xo_sb + l * p.xo_sl;
+    for (int r = 0; r < R; ++r) {
+      const float mean = divide_by(x[r], p.channels, p.inv_channels);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (on[i]) store_row(op + (first + i * 32) * V, v[i]);
+        if (on[i]) add_s<V>(v[r][i], -mean);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum_sq<V>(s, v[r][i]);
+    x[r] = s.x + s.y;
+  }
+  t.template sum<R>(x);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float f = rsqrtf(fmaf(x[r], p.inv_channels, eps));
+#pragma unroll
+    for (int i = 0; i < N; ++i) mul_s<V>(v[r][i], f);
+  }
+}
+
+// What happens to R rows v = x' (unrounded) of a team, tokens l, l + 1 of batch
+// element b, of which those with `keep` are its: x' is written, normed,
+// modulated with the factors that pre(i, a, c) gives, and written as h and in
+// 8 bits.
+template <typename TX, typename TY, int R, int V, int N, bool RES, class Team, class Pre>
+__device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsigned row, int b, int l, int first,
+                                          const bool (&keep)[R], const bool (&on)[N], float (&v)[R][N][V], Pre pre) {
+  if constexpr (RES) {
+    if (p.xo) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!keep[r]) continue;
+        TX* op = static_cast<TX*>(p.xo) + b * p.xo_sb + (l + r) * p.xo_sl + first * V;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (on[i]) store_row(op + i * 32 * V, v[r][i]);
+      }
     }
     if (!p.h && !p.q) return;
   }
-  normalise<V, N>(team, p.pre, p.pre_eps, p, on, v);
+  normalise<R, V, N>(team, p.pre, p.pre_eps, p, on, v);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (!on[i]) continue;
     float a[V], c[V];
     pre(i, a, c);
-    fma_v<V>(v[i], v[i], a, c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) fma_v<V>(v[r][i], v[r][i], a, c);
   }
   if (p.h) {
-    TY* hp = static_cast<TY*>(p.h) + b * p.h_sb + l * p.h_sl;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (on[i]) store_row(hp + (first + i * 32) * V, v[i]);
+    for (int r = 0; r < R; ++r) {
+      if (!keep[r]) continue;
+      TY* hp = static_cast<TY*>(p.h) + b * p.h_sb + (l + r) * p.h_sl + first * V;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (on[i]) store_row(hp + i * 32 * V, v[r][i]);
+    }
   }
   if (p.q) {
-    uint32_t m = 0;
+    float amax[R];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int r = 0; r < R; ++r) {
+      float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (on[i]) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-    const float amax = __uint_as_float(team_max(team, m));
-    // q = h * (127 / amax).  A row of zeros has the scale 0; of one with an
-    // infinity or a NaN the scale is not finite.  Both get the factor 0, and
-    // what is NaN then becomes 0 as a whole number.  Below 2^-120 the row is
-    // scaled up first, as 127 / amax would overflow.
-    const bool tiny = amax < 0x1p-120f;
-    if (tiny) {
+      for (int i = 0; i < N; ++i) {
+        if (!on[i]) continue;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mul_s<V>(v[i], 0x1p100f);
-    }
-    const float up = amax > 0.f && amax <= 3.402823466e38f ? 127.f / (tiny ? amax * 0x1p100f : amax) : 0.f;
-    int8_t* qp = p.q + row * p.q_sl;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (!on[i]) continue;
-      mul_s<V>(v[i], up);
-      if constexpr (V == 8) {
-        int k[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) k[j] = __float2int_rn(v[i][j]);
-        *reinterpret_cast<uint2*>(qp + (first + i * 32) * 8) =
-            make_uint2(pack_s8(k[0], k[1], k[2], k[3]), pack_s8(k[4], k[5], k[6], k[7]));
-      } else {
-        qp[first + i * 32] = static_cast<int8_t>(__float2int_rn(v[i][0]));
+        for (int j = 0; j < V; j += 2) m = max_abs3(m, v[r][i][j], V > 1 ? v[r][i][j + V / 8] : 0.f);
       }
+      amax[r] = m;
     }
-    if (first == 0) p.q_scale[row] = amax / 127.f;
+    team.template max<R>(amax);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!keep[r]) continue;
+      // q = h * (127 / amax).  A row of zeros has the scale 0 and zeros; one
+      // with an infinity or a NaN a scale that is not finite, and zeros too.
+      // Below 2^-120 the row is scaled up first, as 127 / amax would overflow.
+      float up = 0.f;
+      if (amax[r] >= 0x1p-120f && amax[r] <= 3.402823466e38f) {
+        up = 127.f / amax[r];
+      } else {
+        const bool tiny = amax[r] > 0.f && amax[r] < 0x1p-120f;
+        if (tiny) up = 127.f / (amax[r] * 0x1p100f);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[r][i][j] = tiny ? v[r][i][j] * 0x1p100f : 0.f;
+      }
+      int8_t* qp = p.q + (row + r) * p.q_sl + first * V;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (on[i]) store_s8<V>(qp + i * 32 * V, v[r][i], up);
+      if (first == 0) p.q_scale[row + r] = amax[r] / 127.f;
+    }
   }
 }
 
 // Few rows, short groups, rows that vectors cannot read.  One team to a row;
 // each warp has 32 N consecutive vectors of V elements, each thread N of them
 // and, in registers, the folded factors of its channels, which it folds anew
-// where the group changes.  A
-// team goes through consecutive rows and asks for the next one as soon as it
-// has taken the present one out of the load registers, before its sums.
+// where the group changes.  A team goes through consecutive rows and asks for
+// the next one as soon as it has taken the present one out of the load
+// registers, before its sums.
 template <typename TX, typename TY, int V, int N, bool RES, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ __align__(16) float slots[team_slots(THREADS, 1)];
-  Team team;
-  make_team<1>(team, p.warps, slots, team_slots(THREADS, 1));
+  using Team1 = Team<THREADS / 32, 1>;
+  __shared__ __align__(16) float slots[Team1::shared(128, 0)];   // more than one team: 128 threads
+  Team1 team;
+  team.make(p.warps, slots, Team1::shared(128, 0));
   const int teams = blockDim.x / 32 / p.warps;
   const int first = team.warp * 32 * N + threadIdx.x % 32;   // this thread's vectors: first, first + 32, ...
   const int nvec = p.C / V;
@@ -279,30 +314,31 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant_
       of = b;
       until = l - l % p.group + p.group;
     }
-    float v[N][V];
+    float v[1][N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (on[i]) {
-        if constexpr (RES) widen(ry[i], v[i]);
-        else widen(rx[i], v[i]);
+        if constexpr (RES) widen(ry[i], v[0][i]);
+        else widen(rx[i], v[0][i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+        for (int j = 0; j < V; ++j) v[0][i][j] = 0.f;
       }
     }
     if constexpr (RES) {
-      normalise<V, N>(team, p.post, p.post_eps, p, on, v);
+      normalise<1, V, N>(team, p.post, p.post_eps, p, on, v);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (!on[i]) continue;
         float x[V];
         widen(rx[i], x);
-        fma_v<V>(v[i], v[i], PA[i], PB[i]);
-        fma_s<V>(v[i], x, p.rs, v[i]);
+        fma_v<V>(v[0][i], v[0][i], PA[i], PB[i]);
+        fma_s<V>(v[0][i], x, p.rs, v[0][i]);
       }
     }
     if (row + 1 < end) load(row + 1);
-    emit_row<TX, TY, V, N, RES>(p, team, row, b, l, first, on, v, [&](int i, float(&a)[V], float(&c)[V]) {
+    const bool keep[1] = {true};
+    emit_rows<TX, TY, 1, V, N, RES>(p, team, row, b, l, first, keep, on, v, [&](int i, float(&a)[V], float(&c)[V]) {
 #pragma unroll
       for (int j = 0; j < V; ++j) a[j] = A[i][j], c[j] = Bv[i][j];
     });
@@ -310,42 +346,52 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant_
 }
 
 // Many rows of long groups.  The block folds the factors of a group into
-// shared memory and its teams, each with every teams-th row of the block's
-// share, read them from there.  Rows come through a ring of p.depth stages in
-// shared memory by asynchronous copies, each warp's part by that warp: rows on
-// their way cost no registers, and no barrier but the warp's own.
-template <typename TX, typename TY, int N, bool RES, bool FULL, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const __grid_constant__ NormParams p) {
+// shared memory and its teams, each with every teams-th R rows of the block's
+// share, read them from there, once for R rows.  Rows come through a ring of
+// p.depth stages of R rows in shared memory by asynchronous copies, each
+// warp's part by that warp: rows on their way cost no registers, and no
+// barrier but the warp's own.  FULL: the teams' threads have exactly the row's
+// vectors.  R rows that a group's end divides are taken twice, once with each
+// group's factors, and each of them is kept once.
+template <typename TX, typename TY, int R, int N, bool RES, bool FULL, int WARPS>
+__global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormParams p) {
   constexpr int V = 8;
-  constexpr int kX = N * 32 * V * sizeof(TX), kY = RES ? N * 32 * V * sizeof(TY) : 0;   // bytes of a warp's stage
+  constexpr int kX = N * 32 * V * sizeof(TX), kY = RES ? N * 32 * V * sizeof(TY) : 0;   // bytes of a warp's row
+  constexpr int kStage = R * (kX + kY);
+  using TeamR = Team<WARPS, R>;
+  constexpr int kTeamSlots = TeamR::shared(kNormRingThreads, 1);
   extern __shared__ __align__(16) float factors[];
-  __shared__ __align__(16) float slots[team_slots(THREADS, 1)];
-  Team team;
-  make_team<1>(team, p.warps, slots, team_slots(THREADS, 1));
+  __shared__ __align__(16) float slots[kTeamSlots];
+  TeamR team;
+  team.make(p.warps, slots, kTeamSlots);
   const int lane = threadIdx.x % 32;
-  const int teams = blockDim.x / 32 / p.warps;
-  const int first = team.warp * 32 * N + threadIdx.x % 32;   // this thread's vectors: first, first + 32, ...
+  const int teams = blockDim.x / 32 / team.warps;
+  const int first = team.warp * 32 * N + lane;
   const int nvec = p.C / V;
   const unsigned L = p.L, rows = p.B * L;   // below 2^31
   const int planes = RES ? (p.post_bias.p ? 4 : 3) : 2;
-  uint8_t* ring = reinterpret_cast<uint8_t*>(factors + planes * p.C) + (threadIdx.x / 32) * p.depth * (kX + kY);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(factors + planes * p.C) + (threadIdx.x / 32) * p.depth * kStage;
 
   bool on[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) on[i] = first + i * 32 < nvec;
+  for (int i = 0; i < N; ++i) on[i] = FULL || first + i * 32 < nvec;
 
   const unsigned begin = static_cast<unsigned long long>(rows) * blockIdx.x / gridDim.x;
   const unsigned end = static_cast<unsigned long long>(rows) * (blockIdx.x + 1) / gridDim.x;
 
   constexpr int kPieceX = 16 / sizeof(TX), kPieceY = 16 / sizeof(TY);   // channels of a 16-byte piece
   const int c0 = team.warp * 32 * N * V;                                // the warp's first channel
-  // the row that the next copies bring: batch element, token, and whether it is the block's
-  unsigned next = begin + team.index;
+  // the first of the rows that the next copies bring
+  unsigned next = begin + R * team.index;
   int nb = next / L, nl = next - nb * L;
   auto load = [&](int stage) {
-    if (next < end) {
-      const uint32_t dst = smem_u32(ring + stage * (kX + kY)) + lane * 16;
-      const TX* xp = static_cast<const TX*>(p.x) + nb * p.x_sb + nl * p.x_sl;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (next + r >= end) continue;
+      const bool wrap = nl + r >= p.L;   // the row after a batch element's last (R <= 2)
+      const long long b = nb + wrap, l = wrap ? 0 : nl + r;
+      const uint32_t dst = smem_u32(ring + stage * kStage + r * (kX + kY)) + lane * 16;
+      const TX* xp = static_cast<const TX*>(p.x) + b * p.x_sb + l * p.x_sl;
       if (p.x_inner == p.C) {
         const TX* xl = xp + c0 + lane * kPieceX;
 #pragma unroll
@@ -361,11 +407,12 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const __grid_cons
           for (int h = 0; h < V / kPieceX; ++h) {
             const int c = c0 + i * 32 * V + (lane + 32 * h) * kPieceX;
             if (FULL || c < p.C)
-              cp_async_16(dst + i * 32 * V * sizeof(TX) + 512 * h, xp + (c / p.x_inner) * p.x_sh + c % p.x_inner);
+              cp_async_16(dst + i * 32 * V * sizeof(TX) + 512 * h,
+                          xp + (c >> p.inner_shift) * p.x_sh + (c & ((1 << p.inner_shift) - 1)));
           }
       }
       if constexpr (RES) {
-        const TY* yl = static_cast<const TY*>(p.y) + nb * p.y_sb + nl * p.y_sl + c0 + lane * kPieceY;
+        const TY* yl = static_cast<const TY*>(p.y) + b * p.y_sb + l * p.y_sl + c0 + lane * kPieceY;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -373,14 +420,14 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const __grid_cons
             if (FULL || c0 + i * 32 * V + (lane + 32 * h) * kPieceY < p.C)
               cp_async_16(dst + kX + i * 32 * V * sizeof(TY) + 512 * h, yl + i * 32 * V + 32 * h * kPieceY);
       }
-      next += teams;
-      nl += teams;
-      while (nl >= p.L) nl -= p.L, ++nb;
     }
+    next += R * teams;
+    nl += R * teams;
+    while (nl >= p.L && next < end) nl -= p.L, ++nb;
     cp_async_commit();   // also where there is nothing to copy: groups are counted
   };
 
-  unsigned row = begin + team.index;
+  unsigned row = begin + R * team.index;
   for (int s = 0; s < p.depth; ++s) load(s);
   int stage = 0;
   for (unsigned s0 = begin; s0 < end;) {
@@ -400,51 +447,63 @@ __global__ void __launch_bounds__(THREADS, 1) norm_ring_kernel(const __grid_cons
       }
     }
     __syncthreads();
-    for (; row < s1; row += teams) {
-      // all but the depth - 1 youngest groups are complete: this row has come
+    while (row < s1) {
+      // all but the depth - 1 youngest groups are complete: these rows have come
       if (p.depth == 1) cp_async_wait<0>();
       else if (p.depth == 2) cp_async_wait<1>();
       else if (p.depth == 3) cp_async_wait<2>();
       else cp_async_wait<3>();
       __syncwarp();
-      const uint8_t* src = ring + stage * (kX + kY);
-      float v[N][V];
+      const uint8_t* src = ring + stage * kStage;
+      bool keep[R];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (on[i]) {
-          if constexpr (RES) take_staged<TY>(src + kX, i * 32 + lane, v[i]);
-          else take_staged<TX>(src, i * 32 + lane, v[i]);
-        } else {
+      for (int r = 0; r < R; ++r) keep[r] = R == 1 || (row + r >= s0 && row + r < s1);
+      float v[R][N][V];
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (on[i]) {
+            if constexpr (RES) take_staged<TY>(src + r * (kX + kY) + kX, i * 32 + lane, v[r][i]);
+            else take_staged<TX>(src + r * (kX + kY), i * 32 + lane, v[r][i]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[r][i][j] = 0.f;
+          }
         }
       }
       if constexpr (RES) {
-        normalise<V, N>(team, p.post, p.post_eps, p, on, v);
+        normalise<R, V, N>(team, p.post, p.post_eps, p, on, v);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           if (!on[i]) continue;
-          float x[V], a[V];
+          float a[V], c[V];
           get_factor<V>(factors + 2 * p.C, nvec, first + i * 32, a);
-          if (p.post_bias.p) {
-            float c[V];
-            get_factor<V>(factors + 3 * p.C, nvec, first + i * 32, c);
-            fma_v<V>(v[i], v[i], a, c);
-          } else {
-            mul_v<V>(v[i], a);
+          if (p.post_bias.p) get_factor<V>(factors + 3 * p.C, nvec, first + i * 32, c);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float x[V];
+            if (p.post_bias.p) fma_v<V>(v[r][i], v[r][i], a, c);
+            else mul_v<V>(v[r][i], a);
+            take_staged<TX>(src + r * (kX + kY), i * 32 + lane, x);
+            fma_s<V>(v[r][i], x, p.rs, v[r][i]);
           }
-          take_staged<TX>(src, i * 32 + lane, x);
-          fma_s<V>(v[i], x, p.rs, v[i]);
         }
       }
-      __syncwarp();   // all lanes have read the stage
-      load(stage);
-      stage = stage + 1 == p.depth ? 0 : stage + 1;
-      emit_row<TX, TY, V, N, RES>(p, team, row, b, l0 + (row - s0), first, on, v,
-                                  [&](int i, float(&a)[V], float(&c)[V]) {
-                                    get_factor<V>(factors, nvec, first + i * 32, a);
-                                    get_factor<V>(factors + p.C, nvec, first + i * 32, c);
-                                  });
+      const bool again = R > 1 && row + R > s1 && s1 < end;   // some of these rows are the next group's
+      const unsigned this_row = row;
+      if (!again) {
+        __syncwarp();   // all lanes have read the stage
+        load(stage);
+        stage = stage + 1 == p.depth ? 0 : stage + 1;
+        row += R * teams;
+      }
+      emit_rows<TX, TY, R, V, N, RES>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
+                                      [&](int i, float(&a)[V], float(&c)[V]) {
+                                        get_factor<V>(factors, nvec, first + i * 32, a);
+                                        get_factor<V>(factors + p.C, nvec, first + i * 32, c);
+                                      });
+      if (again) break;
     }
     s0 = s1;
   }

@@ -104,18 +104,20 @@ __device__ __forceinline__ void rope_turn(float (&a)[8], const float4& cs, const
 // the norm and for the rotation.  The cosines and sines of a token are made by
 // the team's first threads; their buffers alternate, so that the barrier of
 // the norm's sum is the only one.
-template <typename T, bool HALF>
+template <typename T, bool HALF, int WARPS>
 __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int VECS = HALF ? 2 : 1, N = kRopeVectors / VECS;
   constexpr int kPieces = sizeof(T) / 2;                   // 16-byte pieces of a vector
   constexpr int kTensor = kRopeVectors * 32 * 8 * sizeof(T);   // bytes of a warp's part of a tensor
   extern __shared__ __align__(16) float smem[];
   __shared__ double turns[kRopeMaxD / 2];
-  __shared__ __align__(16) float slots[team_slots(kRopeThreads, 2)];
-  Team team;
-  make_team<2>(team, p.warps, slots, team_slots(kRopeThreads, 2));
+  using Team2 = Team<WARPS, 2>;
+  constexpr int kTeamSlots = Team2::shared(kRopeThreads, WARPS == 1 ? 0 : WARPS == 16 ? 8 : 1);
+  __shared__ __align__(16) float slots[kTeamSlots];
+  Team2 team;
+  team.make(p.warps, slots, kTeamSlots);
   const int lane = threadIdx.x % 32;
-  const int teams = blockDim.x / 32 / p.warps;
+  const int teams = blockDim.x / 32 / team.warps;
   const int tid = team.warp * 32 + lane;
   const int d2 = p.d / 2;
   const int per_head = p.d / (8 * VECS);   // items of a head
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
     float* table = table0 + parity * p.team_floats;
     float* sums = table + p.d;
     parity ^= 1;
-    for (int i = tid; i < d2; i += p.warps * 32) {
+    for (int i = tid; i < d2; i += team.warps * 32) {
       const double t = rope_position(p, b, l, p.axis[i]) * turns[i];
       float sn, cs;
       sincospif(2.f * static_cast<float>(t - rint(t)), &sn, &cs);
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
         }
       }
       if (p.norm == kRopeNormToken) {
-        team_sum2(team, total[0], total[1]);
+        team.template sum<2>(total);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const float r = rsqrtf(fmaf(total[w], p.inv_channels, p.eps));
@@ -261,14 +263,14 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
             for (int o = per_head / 2; o; o >>= 1) m[w][i] += __shfl_xor_sync(0xFFFFFFFFu, m[w][i], o);
             m[w][i] = rsqrtf(fmaf(m[w][i], p.inv_channels, p.eps));
           }
-        team_sync(team);   // the table is complete
+        team.sync();   // the table is complete
       } else {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int i = 0; i < N; ++i)
             if (on[i]) sums[w * items + first + i * 32] = m[w][i];
-        team_sync(team);   // so are the table and the sums
+        team.sync();   // so are the table and the sums
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
           }
       }
     } else {
-      team_sync(team);   // the table is complete
+      team.sync();   // the table is complete
     }
 
     const long long out0 = (static_cast<long long>(b) * p.H * L + l) * p.d;

@@ -242,13 +242,33 @@ __device__ __forceinline__ void sum_sq(float2& s, const float (&a)[V]) {
   }
 }
 
-// Four values, each within the range, as s8 (the first in the lowest byte).
-__device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
-  uint32_t r;
-  asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
-      : "=r"(r)
-      : "r"(a), "r"(b), "r"(c), "r"(d));
+// Largest absolute value of two and of what was largest; a NaN comes through.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
   return r;
+}
+
+// V values times `up`, to the nearest whole numbers (ties to even), as s8, the
+// first in the lowest byte.  |v * up| <= 127: adding 1.5 * 2^23 leaves the
+// whole number in the low bits of the sum, rounded once.
+template <int V>
+__device__ __forceinline__ void store_s8(int8_t* p, const float (&v)[V], float up) {
+  if constexpr (V == 8) {
+    const float2 u = make_float2(up, up), magic = make_float2(12582912.f, 12582912.f);
+    uint32_t k[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), u, magic);
+      k[j] = __float_as_uint(r.x), k[j + 1] = __float_as_uint(r.y);
+    }
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(__byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410),
+                   __byte_perm(__byte_perm(k[4], k[5], 0x0040), __byte_perm(k[6], k[7], 0x0040), 0x5410));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = static_cast<int8_t>(__float_as_uint(fmaf(v[j], up, 12582912.f)));
+  }
 }
 
 // N vectors of V consecutive parameters, `step` elements apart, whose type is
@@ -299,106 +319,109 @@ __device__ __forceinline__ void load_params(const void* p, int dtype, long long 
 }
 
 // ------------------------------------------------------------------ teams
-// A team is `warps` whole warps of a block, numbered from 0; a block holds up
-// to 15 teams of more than one warp (each has a named barrier of its own,
-// barrier 0 being the block's).  Every warp of a team takes the same calls.
-// Its warps meet in two rows of `padded` slots of W floats, which alternate:
-// one barrier a reduction is enough then, as a warp that is one reduction
-// ahead writes the other row, and it cannot be two ahead.  Slots past the last
-// warp's stay zero, so that four are read at a time.
+// A team is WARPS whole warps of a block at most, numbered from 0 (WARPS = 1:
+// one); a block holds up to 15 teams of more than one warp (each has a named
+// barrier of its own, barrier 0 being the block's).  Every warp of a team takes
+// the same calls.  Its warps meet in two rows of kSlots slots of W floats,
+// which alternate: one barrier a reduction is enough then, as a warp that is
+// one reduction ahead writes the other row, and it cannot be two ahead.  Slots
+// past the last warp's stay zero, so that all are read without a count.
+template <int WARPS, int W>
 struct Team {
+  static constexpr int kSlots = (WARPS + 3) / 4 * 4;
   int warps;      // warps of a team
   int index;      // this team's number in the block
   int warp;       // this warp's number in the team
-  int padded;     // warps, rounded up to four
   float* slots;   // the row that the next reduction writes
   float* other;
+
+  // Shared floats (16-byte aligned) of a block of `threads` threads whose teams
+  // have more than WARPS / 2 warps, or more than `least`.
+  static constexpr int shared(int threads, int least) {
+    return WARPS == 1 ? 4 : 2 * W * kSlots * (threads / 32 / (least + 1) + 1);
+  }
+  // The slots are cleared here: the caller has the block synchronise before
+  // the first reduction.
+  __device__ __forceinline__ void make(int warps_, float* all, int count) {
+    warps = WARPS == 1 ? 1 : warps_;
+    index = (threadIdx.x / 32) / warps;
+    warp = (threadIdx.x / 32) % warps;
+    if constexpr (WARPS > 1) {
+      slots = all + 2 * W * kSlots * index;
+      other = slots + W * kSlots;
+      for (int i = threadIdx.x; i < count; i += blockDim.x) all[i] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void sync() const {
+    if (WARPS == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
+  }
+  __device__ __forceinline__ float* turn() {
+    float* s = slots;
+    slots = other;
+    other = s;
+    return s;
+  }
+
+  // Sums over the team, the same bits in every thread and on every run: lanes
+  // by a butterfly, warps in a fixed order.  What a warp of the team wrote to
+  // shared memory before, all of them can read behind it.
+  template <int R>
+  __device__ __forceinline__ void sum(float (&x)[R]) {
+    static_assert(R <= W, "slots");
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], o);
+    if constexpr (WARPS == 1) {
+      __syncwarp();
+      return;
+    } else {
+      float* s = turn();
+      if ((threadIdx.x & 31) == 0) {
+        if constexpr (R == 2) *reinterpret_cast<float2*>(s + 2 * warp) = make_float2(x[0], x[1]);
+        else s[warp] = x[0];
+      }
+      sync();
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSlots; i += 4 / R) {
+        const float4 f = *reinterpret_cast<const float4*>(s + R * i);
+        if constexpr (R == 2) x[0] += f.x + f.z, x[1] += f.y + f.w;
+        else x[0] += (f.x + f.y) + (f.z + f.w);
+      }
+    }
+  }
+  // Largest of absolute values; their bit patterns compare as they do, with a
+  // NaN's above infinity's, so that a NaN anywhere comes through.
+  template <int R>
+  __device__ __forceinline__ void max(float (&x)[R]) {
+    static_assert(R <= W, "slots");
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      x[r] = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x[r]) & 0x7FFFFFFFu));
+    if constexpr (WARPS > 1) {
+      float* s = turn();
+      if ((threadIdx.x & 31) == 0) {
+        if constexpr (R == 2) *reinterpret_cast<float2*>(s + 2 * warp) = make_float2(x[0], x[1]);
+        else s[warp] = x[0];
+      }
+      sync();
+      uint32_t m[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) m[r] = 0;
+#pragma unroll
+      for (int i = 0; i < kSlots; i += 4 / R) {
+        const uint4 f = *reinterpret_cast<const uint4*>(s + R * i);
+        if constexpr (R == 2) m[0] = ::max(m[0], ::max(f.x, f.z)), m[1] = ::max(m[1], ::max(f.y, f.w));
+        else m[0] = ::max(::max(m[0], ::max(f.x, f.y)), ::max(f.z, f.w));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = __uint_as_float(m[r]);
+    }
+  }
 };
-
-// Shared floats of a block of `threads` threads for reductions of W values.
-constexpr int team_slots(int threads, int W) { return 4 * W * (threads / 32) + 16; }
-
-// The slots (16-byte aligned, team_slots() of them) are cleared here: the
-// caller has the block synchronise before the first reduction.
-template <int W>
-__device__ __forceinline__ void make_team(Team& t, int warps, float* slots, int count) {
-  t.warps = warps;
-  t.index = (threadIdx.x / 32) / warps;
-  t.warp = (threadIdx.x / 32) % warps;
-  t.padded = (warps + 3) / 4 * 4;
-  t.slots = slots + 2 * W * t.padded * (warps > 1 ? t.index : 0);
-  t.other = t.slots + W * t.padded;
-  for (int i = threadIdx.x; i < count; i += blockDim.x) slots[i] = 0.f;
-}
-
-__device__ __forceinline__ void team_sync(const Team& t) {
-  if (t.warps == 1) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(t.index + 1), "r"(t.warps * 32) : "memory");
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  return x;
-}
-
-// Sum over the team, the same bits in every thread and on every run: lanes by
-// a butterfly, warps in a fixed order.
-__device__ __forceinline__ float team_sum(Team& t, float x) {
-  x = warp_sum(x);
-  if (t.warps == 1) return x;
-  float* s = t.slots;
-  t.slots = t.other;
-  t.other = s;
-  if ((threadIdx.x & 31) == 0) s[t.warp] = x;
-  team_sync(t);
-  float r = 0.f;
-  for (int i = 0; i < t.padded; i += 4) {
-    const float4 f = *reinterpret_cast<const float4*>(s + i);
-    r += (f.x + f.y) + (f.z + f.w);
-  }
-  return r;
-}
-
-// Two sums at once (W = 2).  What a warp of the team wrote to shared memory
-// before it, all of them can read behind it.
-__device__ __forceinline__ void team_sum2(Team& t, float& x, float& y) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
-  }
-  if (t.warps == 1) return team_sync(t);
-  float* s = t.slots;
-  t.slots = t.other;
-  t.other = s;
-  if ((threadIdx.x & 31) == 0) *reinterpret_cast<float2*>(s + 2 * t.warp) = make_float2(x, y);
-  team_sync(t);
-  x = y = 0.f;
-  for (int i = 0; i < t.padded; i += 2) {
-    const float4 f = *reinterpret_cast<const float4*>(s + 2 * i);
-    x += f.x + f.z;
-    y += f.y + f.w;
-  }
-}
-
-// Maximum of bit patterns.  Of absolute values it is the largest one, and a
-// NaN's pattern is above that of infinity, so a NaN anywhere comes through.
-__device__ __forceinline__ uint32_t team_max(Team& t, uint32_t x) {
-  x = __reduce_max_sync(0xFFFFFFFFu, x);
-  if (t.warps == 1) return x;
-  float* s = t.slots;
-  t.slots = t.other;
-  t.other = s;
-  if ((threadIdx.x & 31) == 0) s[t.warp] = __uint_as_float(x);
-  team_sync(t);
-  uint32_t r = 0;
-  for (int i = 0; i < t.padded; i += 4) {
-    const uint4 f = *reinterpret_cast<const uint4*>(s + i);
-    r = max(max(r, f.x), max(f.y, max(f.z, f.w)));
-  }
-  return r;
-}
 
 // x / n for n = 1 / inv: a product and a correction of its error, so that the
 // mean of equal values is that value.
