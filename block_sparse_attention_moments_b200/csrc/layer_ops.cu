@@ -137,9 +137,9 @@ int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_
   constexpr int R = kNormRingRows<TX, RES>, N = kNormRingVectors;
   const int teams = p.warps > 1 ? std::min(15, kNormRingThreads / 32 / p.warps) : kNormRingThreads / 32;
   const size_t row = static_cast<size_t>(p.warps) * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-  const int fit = static_cast<int>((kNormRingShared - factors) / (R * row));   // stages of all teams
+  const int fit = R == 1 ? teams : static_cast<int>((kNormRingShared - factors) / (R * row));   // stages of all teams
   const int used = std::min(teams, fit);
-  p.depth = std::min(4, fit / used);
+  p.depth = R == 1 ? 0 : std::min(4, fit / used);
   static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
   if (!attr_set[dev]) {
     CUDA_TRY(cudaFuncSetAttribute(norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>,
@@ -164,7 +164,7 @@ bool for_norm_ring(NormParams& p, size_t* factors, int sms) {
   for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
   return rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
          (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift) &&
-         *factors + 2 * kNormRingRows<TX, RES> * row <= kNormRingShared;
+         *factors + (kNormRingRows<TX, RES> == 1 ? 0 : 4 * row) <= kNormRingShared;
 }
 
 template <typename TX, typename TY, bool RES>

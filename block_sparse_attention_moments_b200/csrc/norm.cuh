@@ -347,16 +347,22 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant_
 
 // Many rows of long groups.  The block folds the factors of a group into
 // shared memory and its teams, each with every teams-th R rows of the block's
-// share, read them from there, once for R rows.  Rows come through a ring of
-// p.depth stages of R rows in shared memory by asynchronous copies, each
-// warp's part by that warp: rows on their way cost no registers, and no
-// barrier but the warp's own.  FULL: the teams' threads have exactly the row's
-// vectors.  R rows that a group's end divides are taken twice, once with each
-// group's factors, and each of them is kept once.
+// share, read them from there, once for R rows.  With R = 2 the rows come
+// through a ring of p.depth stages of R rows in shared memory by asynchronous
+// copies, each warp's part by that warp: rows on their way cost no registers,
+// and no barrier but the warp's own.  With R = 1 (an fp32 stream and a block's
+// output, whose factors leave little room) the next row is on its way in
+// registers: 75600 x 5120, fp32 and bf16, takes 739 us so and 830 through the
+// ring; the bf16 norm alone takes 362 us in registers and 288 through the ring.
+// FULL: the teams' threads have exactly the row's vectors.  R rows that a
+// group's end divides are taken twice, once with each group's factors, and
+// each of them is kept once.
+// (R = 1 only with RES.)
 template <typename TX, typename TY, int R, int N, bool RES, bool FULL, int WARPS>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormParams p) {
   constexpr int V = 8;
   constexpr int kX = N * 32 * V * sizeof(TX), kY = RES ? N * 32 * V * sizeof(TY) : 0;   // bytes of a warp's row
+  constexpr bool RING = R > 1;
   constexpr int kStage = R * (kX + kY);
   using TeamR = Team<WARPS, R>;
   constexpr int kTeamSlots = TeamR::shared(kNormRingThreads, 1);
@@ -379,12 +385,32 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
   const unsigned begin = static_cast<unsigned long long>(rows) * blockIdx.x / gridDim.x;
   const unsigned end = static_cast<unsigned long long>(rows) * (blockIdx.x + 1) / gridDim.x;
 
-  constexpr int kPieceX = 16 / sizeof(TX), kPieceY = 16 / sizeof(TY);   // channels of a 16-byte piece
-  const int c0 = team.warp * 32 * N * V;                                // the warp's first channel
-  // the first of the rows that the next copies bring
+  // the first of the rows that are to be fetched next
   unsigned next = begin + R * team.index;
   int nb = next / L, nl = next - nb * L;
+  auto advance = [&]() {
+    next += R * teams;
+    nl += R * teams;
+    while (nl >= p.L && next < end) nl -= p.L, ++nb;
+  };
+  Raw<TX, V> rx[RING ? 1 : N];   // without a ring: the row on its way
+  Raw<TY, V> ry[RING ? 1 : N];
   auto load = [&](int stage) {
+    if constexpr (!RING) {
+      if (next < end) {
+        const TX* xp = static_cast<const TX*>(p.x) + nb * p.x_sb + nl * p.x_sl + first * V;
+        const TY* yp = static_cast<const TY*>(p.y) + nb * p.y_sb + nl * p.y_sl + first * V;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (on[i]) load_raw(rx[i], xp + i * 32 * V);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (on[i]) load_raw(ry[i], yp + i * 32 * V);
+      }
+      return advance();
+    }
+    constexpr int kPieceX = 16 / sizeof(TX), kPieceY = 16 / sizeof(TY);   // channels of a 16-byte piece
+    const int c0 = team.warp * 32 * N * V;                                // the warp's first channel
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (next + r >= end) continue;
@@ -421,14 +447,12 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
               cp_async_16(dst + kX + i * 32 * V * sizeof(TY) + 512 * h, yl + i * 32 * V + 32 * h * kPieceY);
       }
     }
-    next += R * teams;
-    nl += R * teams;
-    while (nl >= p.L && next < end) nl -= p.L, ++nb;
+    advance();
     cp_async_commit();   // also where there is nothing to copy: groups are counted
   };
 
   unsigned row = begin + R * team.index;
-  for (int s = 0; s < p.depth; ++s) load(s);
+  for (int s = 0; s < (RING ? p.depth : 1); ++s) load(s);
   int stage = 0;
   for (unsigned s0 = begin; s0 < end;) {
     const int b = s0 / L;
@@ -448,13 +472,15 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     }
     __syncthreads();
     while (row < s1) {
-      // all but the depth - 1 youngest groups are complete: these rows have come
-      if (p.depth == 1) cp_async_wait<0>();
-      else if (p.depth == 2) cp_async_wait<1>();
-      else if (p.depth == 3) cp_async_wait<2>();
-      else cp_async_wait<3>();
-      __syncwarp();
-      const uint8_t* src = ring + stage * kStage;
+      if constexpr (RING) {
+        // all but the depth - 1 youngest groups are complete: these rows have come
+        if (p.depth == 1) cp_async_wait<0>();
+        else if (p.depth == 2) cp_async_wait<1>();
+        else if (p.depth == 3) cp_async_wait<2>();
+        else cp_async_wait<3>();
+        __syncwarp();
+      }
+      [[maybe_unused]] const uint8_t* src = ring + stage * kStage;
       bool keep[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) keep[r] = R == 1 || (row + r >= s0 && row + r < s1);
@@ -464,7 +490,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           if (on[i]) {
-            if constexpr (RES) take_staged<TY>(src + r * (kX + kY) + kX, i * 32 + lane, v[r][i]);
+            if constexpr (!RING) widen(ry[i], v[r][i]);
+            else if constexpr (RES) take_staged<TY>(src + r * (kX + kY) + kX, i * 32 + lane, v[r][i]);
             else take_staged<TX>(src + r * (kX + kY), i * 32 + lane, v[r][i]);
           } else {
 #pragma unroll
@@ -485,7 +512,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
             float x[V];
             if (p.post_bias.p) fma_v<V>(v[r][i], v[r][i], a, c);
             else mul_v<V>(v[r][i], a);
-            take_staged<TX>(src + r * (kX + kY), i * 32 + lane, x);
+            if constexpr (RING) take_staged<TX>(src + r * (kX + kY), i * 32 + lane, x);
+            else widen(rx[i], x);
             fma_s<V>(v[r][i], x, p.rs, v[r][i]);
           }
         }
@@ -493,9 +521,9 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
       const bool again = R > 1 && row + R > s1 && s1 < end;   // some of these rows are the next group's
       const unsigned this_row = row;
       if (!again) {
-        __syncwarp();   // all lanes have read the stage
+        if constexpr (RING) __syncwarp();   // all lanes have read the stage
         load(stage);
-        stage = stage + 1 == p.depth ? 0 : stage + 1;
+        if constexpr (RING) stage = stage + 1 == p.depth ? 0 : stage + 1;
         row += R * teams;
       }
       emit_rows<TX, TY, R, V, N, RES>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     }
     s0 = s1;
   }
-  cp_async_wait<0>();
+  if constexpr (RING) cp_async_wait<0>();
 }
 
 }  // namespace solattn
