@@ -139,7 +139,7 @@ int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_
   const size_t row = static_cast<size_t>(p.warps) * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
   const int fit = R == 1 ? teams : static_cast<int>((kNormRingShared - factors) / (R * row));   // stages of all teams
   const int used = std::min(teams, fit);
-  p.depth = R == 1 ? 0 : std::min(4, fit / used);
+  p.depth = R == 1 ? 1 : std::min(4, fit / used);
   static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
   if (!attr_set[dev]) {
     CUDA_TRY(cudaFuncSetAttribute(norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>,
@@ -147,7 +147,7 @@ int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_
     attr_set[dev] = true;
   }
   norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>
-      <<<sms, used * p.warps * 32, factors + static_cast<size_t>(used) * p.depth * R * row, st>>>(p);
+      <<<sms, used * p.warps * 32, factors + (R == 1 ? 0 : static_cast<size_t>(used) * p.depth * R * row), st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
 }

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const __grid_constant_
 // copies, each warp's part by that warp: rows on their way cost no registers,
 // and no barrier but the warp's own.  With R = 1 (an fp32 stream and a block's
 // output, whose factors leave little room) the next row is on its way in
-// registers: 75600 x 5120, fp32 and bf16, takes 739 us so and 830 through the
+// registers: 75600 x 5120, fp32 and bf16, takes 737 us so and 830 through the
 // ring; the bf16 norm alone takes 362 us in registers and 288 through the ring.
 // FULL: the teams' threads have exactly the row's vectors.  R rows that a
 // group's end divides are taken twice, once with each group's factors, and
@@ -402,12 +402,10 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
         const TY* yp = static_cast<const TY*>(p.y) + nb * p.y_sb + nl * p.y_sl + first * V;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (on[i]) load_raw(rx[i], xp + i * 32 * V);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (on[i]) load_raw(ry[i], yp + i * 32 * V);
+          if (on[i]) load_raw(rx[i], xp + i * 32 * V), load_raw(ry[i], yp + i * 32 * V);
       }
-      return advance();
+      advance();
+      return cp_async_commit();
     }
     constexpr int kPieceX = 16 / sizeof(TX), kPieceY = 16 / sizeof(TY);   // channels of a 16-byte piece
     const int c0 = team.warp * 32 * N * V;                                // the warp's first channel
@@ -452,7 +450,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
   };
 
   unsigned row = begin + R * team.index;
-  for (int s = 0; s < (RING ? p.depth : 1); ++s) load(s);
+  for (int s = 0; s < p.depth; ++s) load(s);
   int stage = 0;
   for (unsigned s0 = begin; s0 < end;) {
     const int b = s0 / L;
@@ -472,14 +470,14 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     }
     __syncthreads();
     while (row < s1) {
-      if constexpr (RING) {
-        // all but the depth - 1 youngest groups are complete: these rows have come
-        if (p.depth == 1) cp_async_wait<0>();
-        else if (p.depth == 2) cp_async_wait<1>();
-        else if (p.depth == 3) cp_async_wait<2>();
-        else cp_async_wait<3>();
-        __syncwarp();
-      }
+      // All but the depth - 1 youngest groups are complete: these rows have come.
+      // (Rows in registers keep the empty groups and the warp's meetings: without
+      // them the compiler's order of the loads costs 7%.)
+      if (p.depth == 1) cp_async_wait<0>();
+      else if (p.depth == 2) cp_async_wait<1>();
+      else if (p.depth == 3) cp_async_wait<2>();
+      else cp_async_wait<3>();
+      __syncwarp();
       [[maybe_unused]] const uint8_t* src = ring + stage * kStage;
       bool keep[R];
 #pragma unroll
@@ -521,9 +519,9 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
       const bool again = R > 1 && row + R > s1 && s1 < end;   // some of these rows are the next group's
       const unsigned this_row = row;
       if (!again) {
-        if constexpr (RING) __syncwarp();   // all lanes have read the stage
+        __syncwarp();   // all lanes have read the stage
         load(stage);
-        if constexpr (RING) stage = stage + 1 == p.depth ? 0 : stage + 1;
+        stage = stage + 1 == p.depth ? 0 : stage + 1;
         row += R * teams;
       }
       emit_rows<TX, TY, R, V, N, RES>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
@@ -535,7 +533,7 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     }
     s0 = s1;
   }
-  if constexpr (RING) cp_async_wait<0>();
+  cp_async_wait<0>();
 }
 
 }  // namespace solattn
