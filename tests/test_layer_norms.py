@@ -375,3 +375,100 @@ def test_refusals():
     refused("eps", lambda: sa.norm_modulate(x, eps=-1.0))
     refused("exceeds", lambda: sa.norm_modulate(randn(1, 16392, dtype=BF16)))
     refused("no channels", lambda: sa.norm_modulate(x[..., :0]))
+
+
+# ------------------------------------------------------------------ many rows
+# From 32 rows of a block on (4736 and more on 148 SMs) another kernel takes the
+# rows, with folded factors in shared memory, two rows at a time and groups whose
+# ends may lie between the two.
+MANY = [(3, 1, 1601, 64), (1, 13, 391, 264), (2, 3, 801, 1024), (5, 1, 1001, 1544), (1, 1, 4737, 2048), (2, 7, 343, 2056),
+        (1, 1, 4800, 5120), (3, 50, 33, 1000), (1, 5, 961, 8192)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,G,per,C", MANY)
+@pytest.mark.parametrize("dtype,ydtype", [(BF16, BF16), (FP16, FP16), (FP32, FP32), (FP32, BF16)])
+def test_many_rows(B, G, per, C, dtype, ydtype):
+    L = G * per
+    x = randn(B, L, C, dtype=dtype, mean=0.3)
+    six = randn(B, G, 6, C, std=0.4)
+    gate, scale, shift = six[:, :, 2], six[:, :, 1], six[:, :, 0]
+    weight, bias = randn(C, dtype=ydtype, mean=1, std=0.2), randn(C, dtype=ydtype)
+    h = sa.norm_modulate(x, scale, shift, norm="layer", weight=weight, bias=bias, out_dtype=ydtype)
+    _, _, want, size = reference(x, scale=scale, shift=shift, weight=weight, bias=bias)
+    close(h, want, size, "h")
+    q, s = sa.norm_modulate(x, scale, shift, norm="rms", quantize=True)
+    _, _, want, size = reference(x, scale=scale, shift=shift, norm="rms")
+    check_quantised(q, s, want, size)
+    y = randn(B, L, C, dtype=ydtype, mean=-0.2)
+    for post, post_bias in (("none", None), ("rms", None), ("layer", bias)):
+        kw = dict(residual_scale=0.5, post_norm=post, post_weight=weight, post_bias=post_bias, norm="rms")
+        want_x, size_x, want, size = reference(x, y, gate, scale, shift, **kw)
+        xn, h = sa.gate_residual_norm(x, y, gate, scale, shift, **kw)
+        close(xn, want_x, size_x, "x'")
+        close(h, want, size, "h")
+    inplace = x.clone()
+    got, h2 = sa.gate_residual_norm(inplace, y, gate, scale, shift, x_out=inplace, **kw)
+    assert torch.equal(got, xn) and torch.equal(h2, h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,d", [(8, 128), (16, 64), (40, 128), (5, 8), (3, 24)])
+def test_many_rows_of_heads(H, d):
+    o = randn(2, H, 2500, d, dtype=BF16)
+    q, s = sa.quantize_rows(o.transpose(1, 2))
+    rows = o.transpose(1, 2).flatten(2)
+    check_quantised(q, s, rows.double(), torch.zeros_like(rows, dtype=torch.float64))
+    q2, s2 = sa.quantize_rows(rows)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [520, 1024, 1544])
+def test_many_rows_do_not_touch_each_other(C):
+    """Bad rows at a pair's first and second place, at a group's and at a batch element's border."""
+    B, G, per = 3, 5, 333
+    x, y = randn(B, G * per, C, dtype=BF16), randn(B, G * per, C, dtype=BF16)
+    scale = randn(B, G, C, std=0.3)
+    clean = sa.gate_residual_norm(x, y, None, scale)
+    clean_q = sa.norm_modulate(x, scale, quantize=True)
+    bad = torch.zeros(B, G * per, dtype=torch.bool, device="cuda")
+    for b, l in ((0, 0), (0, 332), (0, 333), (0, 700), (0, 1664), (1, 0), (1, 999), (1, 1001), (2, 1664)):
+        bad[b, l] = True
+        x[b, l, (7 * l) % C] = math.nan if l % 2 else math.inf
+    xn, h = sa.gate_residual_norm(x, y, None, scale)
+    assert torch.equal(h[~bad], clean[1][~bad]) and torch.equal(xn[~bad], clean[0][~bad]) and h[bad].isnan().all()
+    q, s = sa.norm_modulate(x, scale, quantize=True)
+    assert torch.equal(q[~bad], clean_q[0][~bad]) and torch.equal(s[~bad], clean_q[1][~bad])
+    assert not s[bad].isfinite().any() and not q[bad].any()
+    x[:] = 0
+    q, s = sa.quantize_rows(x)
+    assert not q.any() and not s.any()
+
+
+@pytest.mark.gpu
+def test_many_rows_and_few_give_the_same_values():
+    """The same row through both kernels: each within its tolerance, so they differ by two tolerances at most; and
+    the larger kernel's result does not depend on what comes before or behind a row."""
+    x = randn(1, 6000, 640, dtype=FP32)
+    scale = randn(640, std=0.3)
+    a = sa.norm_modulate(x, scale)
+    assert torch.equal(a[:, 500:5500], sa.norm_modulate(x[:, 500:5500], scale))
+    b = sa.norm_modulate(x[:, :100], scale)
+    _, _, want, size = reference(x[:, :100], scale=scale)
+    close(b, want, size, "few")
+    close(a[:, :100], want, size, "many")
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Rows that lie more than 2^31 elements from the first one, read, written and modulated."""
+    C, L = 8, 6000
+    big = torch.empty(1 + 2 ** 31 // 1024 + 4000, 1024, device="cuda", dtype=BF16)     # 4.3 GB
+    x = big.as_strided((2, L, C), (2 ** 31 + 16, 64, 1))
+    v = randn(2, L, C, dtype=BF16)
+    x.copy_(v)
+    assert torch.equal(sa.norm_modulate(x), sa.norm_modulate(v))
+    out = big.as_strided((2, L, C), (2 ** 31 + 16, 64, 1), 8)
+    sa.norm_modulate(v, out=out)
+    assert torch.equal(out, sa.norm_modulate(v)) and torch.equal(x, v)

@@ -270,3 +270,57 @@ def test_refusals():
     refused("contiguous", lambda: sa.rope(q.transpose(2, 3), k.transpose(2, 3), axes=(0, 0, 2), **kw))
     refused("no backward", lambda: sa.rope(q.clone().requires_grad_(), k, v, **kw))
     refused("CUDA", lambda: sa.rope(q.cpu(), k, v, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pairing", ["interleaved", "half"])
+@pytest.mark.parametrize("norm", ["none", "head", "token"])
+@pytest.mark.parametrize("B,H,d,grid,extra", [(2, 40, 128, (5, 9, 14), 3), (1, 8, 64, (7, 30, 41), 0), (1, 3, 96, (9, 31, 20), 11),
+                                              (1, 70, 96, (3, 20, 13), 0)])
+def test_more_tokens_than_teams(B, H, d, grid, extra, norm, pairing):
+    """Teams that go through several tokens: rings and tables that come round."""
+    L = math.prod(grid) + extra
+    q, k, v = make(B, L, H, d, BF16, 20)
+    wq, wk = weights(norm, H, d, BF16, 21)
+    q2, k2, v2 = sa.rope(q, k, v, grid=grid, pairing=pairing, norm=norm, q_weight=wq, k_weight=wk)
+    pos, axes = grid_positions(L, grid, 0), sa.rope_axes(d)
+    close(q2, reference(q, pos, axes, wq, norm, pairing), "q")
+    close(k2, reference(k, pos, axes, wk, norm, pairing), "k")
+    assert torch.equal(v2, v.transpose(1, 2))
+    q2, k2 = sa.rope(q, k, positions=pos.cuda(), pairing=pairing, norm=norm, q_weight=wq, k_weight=wk)
+    close(k2, reference(k, pos, axes, wk, norm, pairing), "k without v")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", ["head", "token"])
+@pytest.mark.parametrize("H,d", [(64, 256), (341, 48), (68, 240), (1024, 16), (204, 80)])
+def test_the_widest_rows(H, d, norm):
+    """fp32 rows of up to 16384 channels with v: less of them fits shared memory."""
+    q, k, v = make(1, 200, H, d, FP32, 22)
+    wq, wk = weights(norm, H, d, FP32, 23)
+    for pairing in ("interleaved", "half"):
+        q2, k2, v2 = sa.rope(q, k, v, grid=(4, 5, 10), pairing=pairing, norm=norm, q_weight=wq, k_weight=wk)
+        pos, axes = grid_positions(200, (4, 5, 10), 0), sa.rope_axes(d)
+        close(q2, reference(q, pos, axes, wq, norm, pairing), "q")
+        close(k2, reference(k, pos, axes, wk, norm, pairing), "k")
+        assert torch.equal(v2, v.transpose(1, 2))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Inputs whose tokens and heads lie more than 2^31 elements from the first one, and an output of that size."""
+    B, L, H, d = 1, 40, 2, 64
+    big = torch.zeros(2 ** 31 // 1024 + 8000, 1024, device="cuda", dtype=BF16)
+    q, k, v = make(B, L, H, d, BF16, 24)
+    far = [big.as_strided((B, L, H, d), (2 ** 31, 64, 2 ** 31 + 4096, 1), i * 8192) for i in range(3)]
+    for f, t in zip(far, (q, k, v)):
+        f.copy_(t)
+    kw = dict(grid=(2, 4, 5), norm="head")
+    assert all(torch.equal(a, b) for a, b in zip(sa.rope(*far, **kw), sa.rope(q, k, v, **kw)))
+    del big, far
+    L = 300_000
+    q = torch.randn(1, 1, 128, 64, device="cuda", dtype=BF16).expand(1, L, 128, 64)     # 2.46e9 values out
+    out, _ = sa.rope(q, q, grid=(300, 40, 25))
+    for l in (0, 1, 262_143, 262_144, L - 1):
+        one, _ = sa.rope(q[:, :1], q[:, :1], grid=(300, 40, 25), start=l)
+        assert torch.equal(out[:, :, l], one[:, :, 0])
