@@ -21,6 +21,7 @@ namespace {
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
 constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
+constexpr int kFewTokens = 128;                   // tokens up to which their tiles of 64 are taken
 constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
 constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
 // Rows of a team at a time: two share the factors' reads and the barriers; of
@@ -180,9 +181,11 @@ int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st
       return full ? launch_norm_ring<TX, TY, RES, true, 8>(r, factors, dev, sms, st)
                   : launch_norm_ring<TX, TY, RES, false, 8>(r, factors, dev, sms, st);
     }
+    if (p.C <= 2816) return launch_norm_as<TX, TY, 8, 1, RES, 352>(p, sms, st);
     if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
     return launch_norm_as<TX, TY, 8, 4, RES, 512>(p, sms, st);
   }
+  if (p.C <= 1408) return launch_norm_as<TX, TY, 1, 4, RES, 352>(p, sms, st);
   if (p.C <= 2560) return launch_norm_as<TX, TY, 1, 4, RES, 640>(p, sms, st);
   if (p.C <= 8192) return launch_norm_as<TX, TY, 1, 16, RES, 512>(p, sms, st);
   return launch_norm_as<TX, TY, 1, 32, RES, 512>(p, sms, st);
@@ -319,8 +322,9 @@ int launch_linear_vec(const LinearParams& p, const LinearOperands& o, int sms, c
 }
 
 template <int BT, typename T>
-int launch_linear_few(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
+int launch_linear_few(LinearParams p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
   using C = FewConfig<BT>;
+  p.tiles_m = (p.M + BT - 1) / BT;
   CUtensorMap ma, mw;
   int rc;
   if ((rc = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.a, p.K, p.M, o.a_pitch, 128, BT))) return rc;
@@ -331,7 +335,7 @@ int launch_linear_few(const LinearParams& p, const LinearOperands& o, int dev, i
                                   static_cast<int>(C::kSmem)));
     attr_set[dev] = true;
   }
-  const int tiles = (p.N + 127) / 128, kblocks = (p.K + 127) / 128;
+  const int tiles = (p.N + 127) / 128 * p.tiles_m, kblocks = (p.K + 127) / 128;
   int log_split = 0;
   while (log_split < 3 && (tiles << log_split) < sms && (2 << log_split) <= kblocks) ++log_split;
   const int split = 1 << log_split;
@@ -357,8 +361,7 @@ int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms,
   if (p.M <= 4) return launch_linear_vec<4, T>(p, o, sms, st);
   if (p.M <= 16) return launch_linear_few<16, T>(p, o, dev, sms, st);
   if (p.M <= 32) return launch_linear_few<32, T>(p, o, dev, sms, st);
-  if (p.M <= 64) return launch_linear_few<64, T>(p, o, dev, sms, st);
-  if (p.M <= 128) return launch_linear_few<128, T>(p, o, dev, sms, st);
+  if (p.M <= kFewTokens) return launch_linear_few<64, T>(p, o, dev, sms, st);
   // The variant whose slowest SM is done first: waves of tiles, each the MMA
   // time of its K (in units of 128 x 128 x 128 of an SM) and the time until
   // the pipeline is full and the last output is written.

@@ -457,17 +457,17 @@ __global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid
     static_cast<T*>(p.out)[m * p.out_pitch + n] = from_f32<T>(linear_value(mine, p.a_scale[m], p.w_scale[n], bias_at(p, n)));
 }
 
-// ------------------------------------------------------------------ up to 128 tokens
+// ------------------------------------------------------------------ few tokens
 // The tile the other way round: 128 channels are the rows of the MMA and BT
-// tokens its columns, so that the weights, which bound it, fill whole tiles.
-// A cluster of `split` CTAs shares a tile's K; each reads its accumulators and
+// tokens its columns, so that the weights, which bound it, fill whole tiles
+// (the tiles of further tokens find them in L2).  A cluster of `split` CTAs shares a tile's K; each reads its accumulators and
 // gives every rank the sums of that rank's tokens through distributed shared
 // memory, where the rank adds them in order.  One tile to a cluster, a few
 // CTAs to an SM.
 template <int BT>
 struct FewConfig {
   static constexpr int kStage = kLinStageA + BT * 128;
-  static constexpr int kStages = BT <= 32 ? 4 : BT == 64 ? 3 : 3;
+  static constexpr int kStages = BT <= 32 ? 4 : 3;
   static constexpr int kParts = BT * 128 * 4;
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kParts + BT * 4 + 256;
 };
@@ -493,7 +493,9 @@ __global__ void __launch_bounds__(kLinThreads)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
-  const int split = 1 << log_split, n0 = (blockIdx.x >> log_split) * 128;
+  const int split = 1 << log_split, tile = blockIdx.x >> log_split;
+  const int n0 = tile / p.tiles_m * 128, t0 = tile % p.tiles_m * BT;   // first channel and token
+  const int tokens = p.M - t0;
   if (split > 1) cluster_arrive();   // met before the first access to another CTA's memory, which must have started
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kLinThreads)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_all<1>(tmem_slot, kTmem);
-  for (int i = threadIdx.x; i < BT; i += kLinThreads) a_scale[i] = i < p.M ? p.a_scale[i] : 0.f;
+  for (int i = threadIdx.x; i < BT; i += kLinThreads) a_scale[i] = i < tokens ? p.a_scale[t0 + i] : 0.f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kLinThreads)
       mbar_arrive_expect_tx(&full[s], C::kStage);
       const uint32_t dst = smem_u32(base + s * C::kStage);
       tma_load_2d<1>(dst, &map_w, smem_u32(&full[s]), k * 128, n0);
-      tma_load_2d<1>(dst + kLinStageA, &map_a, smem_u32(&full[s]), k * 128, 0);
+      tma_load_2d<1>(dst + kLinStageA, &map_a, smem_u32(&full[s]), k * 128, t0);
     }
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = idesc_s8_s32(128, BT);
@@ -575,8 +577,8 @@ __global__ void __launch_bounds__(kLinThreads)
     }
     cluster_sync();
     if (warp >= 2 && n < p.N) {
-      const int m0 = rank * each, count = min(each, p.M - m0);
-      T* o = static_cast<T*>(p.out) + m0 * p.out_pitch + n;
+      const int m0 = rank * each, count = min(each, tokens - m0);
+      T* o = static_cast<T*>(p.out) + (t0 + m0) * p.out_pitch + n;
 #pragma unroll 4
       for (int j = 0; j < count; ++j) {
         int sum = 0;
@@ -585,10 +587,10 @@ __global__ void __launch_bounds__(kLinThreads)
       }
     }
   } else if (warp >= 2 && n < p.N) {
-    T* o = static_cast<T*>(p.out) + n;
+    T* o = static_cast<T*>(p.out) + t0 * p.out_pitch + n;
 #pragma unroll
     for (int j = 0; j < BT; ++j)
-      if (j < p.M) o[j * p.out_pitch] = from_f32<T>(linear_value(r[j], a_scale[j], ws, b));
+      if (j < tokens) o[j * p.out_pitch] = from_f32<T>(linear_value(r[j], a_scale[j], ws, b));
   }
   __syncwarp();
   tc_fence_before();

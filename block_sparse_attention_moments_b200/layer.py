@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import struct
+from operator import index
 
 import torch
 
@@ -116,22 +117,27 @@ def _placed(fn):
         x = args[0] if args else next(iter(kw.values()), None)
         if isinstance(x, torch.Tensor) and x.is_cuda:
             if stream is not None:
-                if stream.device != x.device:
-                    raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-                if stream != torch.cuda.current_stream(x.device):
-                    for t in (*args, *kw.values()):
-                        if isinstance(t, torch.Tensor) and t.is_cuda:
-                            t.record_stream(stream)
-                with torch.cuda.stream(stream):
-                    return fn(*args, **kw)
-            if x.get_device() != torch.cuda.current_device():
+                return on_stream(x, stream, args, kw)
+            if x.get_device() != _current_device():
                 with torch.cuda.device(x.device):
                     return fn(*args, **kw)
         return fn(*args, **kw)
+
+    def on_stream(x, stream, args, kw):
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        if stream != torch.cuda.current_stream(x.device):
+            for t in (*args, *kw.values()):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
     return call
 
 
-# The handle of a device's current stream without a Stream object in between.
+# The current device without torch.cuda's lazy initialisation (a CUDA tensor is at hand), and the handle of a
+# device's current stream without a Stream object in between.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
@@ -278,6 +284,7 @@ def rope_axes(d):
 @functools.lru_cache(maxsize=64)
 def _rope_pairs(axes, theta, freqs, d):
     """The host arrays of a pair's frequency and axis, with their addresses; they depend on plain numbers only."""
+    axes = tuple(index(n) for n in axes)
     if any(n < 0 or n % 2 for n in axes) or sum(axes) != d:
         raise ValueError(f"axes must be {len(axes)} even numbers that sum to {d} (got {axes})")
     axis = [i for i, n in enumerate(axes) for _ in range(n // 2)]
@@ -334,11 +341,17 @@ def rope(q, k, v=None, *, grid=None, positions=None, axes=None, start=0, theta=1
         raise ValueError("give either grid or positions")
     A = 3
     if grid is not None:
-        if len(grid) != 3 or any(int(n) != n or not 1 <= n < 2 ** 31 for n in grid):
+        try:
+            F, R, C = grid
+            F, R, C = index(F), index(R), index(C)
+        except (TypeError, ValueError):
+            F = 0
+        if F < 1 or R < 1 or C < 1 or F >= 2 ** 31 or R >= 2 ** 31 or C >= 2 ** 31:
             raise ValueError(f"grid must be (frames, rows, columns), each at least 1 (got {grid!r})")
+        start = index(start)
         if not 0 <= start < 2 ** 62:
             raise ValueError(f"start must not be negative (got {start!r})")
-        where = (0, int(grid[0]), int(grid[1]), int(grid[2]), start, 0, 0, 0, 0)
+        where = (0, F, R, C, start, 0, 0, 0, 0)
     else:
         _input(positions, "positions", dev, _POSITIONS)
         shape, strides = positions.shape, positions.stride()
@@ -353,20 +366,19 @@ def rope(q, k, v=None, *, grid=None, positions=None, axes=None, start=0, theta=1
         if A != 3:
             raise ValueError(f"axes must be given for {A} axes")
         axes = rope_axes(d)
-    axes = tuple(int(n) for n in axes)
     if len(axes) != A:
-        raise ValueError(f"axes must be {A} even numbers that sum to {d} (got {axes})")
-    freq_ptr, axis_ptr, *keep = _rope_pairs(axes, float(theta), None if freqs is None else tuple(float(f) for f in freqs), d)
+        raise ValueError(f"axes must be {A} even numbers that sum to {d} (got {tuple(axes)})")
+    pairs = _rope_pairs(tuple(axes), float(theta), None if freqs is None else tuple(map(float, freqs)), d)
     n = 0 if kind == 0 else d if kind == 1 else H * d
-    outs = [q.new_empty((B, H, L, d)) for _ in range(2 if v is None else 3)]
+    outs = (q.new_empty((B, H, L, d)), q.new_empty((B, H, L, d))) + (() if v is None else (q.new_empty((B, H, L, d)),))
     tensors = _rope_tensor(q, "q", q, q_weight, n, outs[0]) + _rope_tensor(k, "k", q, k_weight, n, outs[1])
     tensors += (0, 0, 0, 0, 0, 0, 0) if v is None else _rope_tensor(v, "v", q, None, n, outs[2])
     if B and L and H:
-        args = _ROPE_ARGS.pack(B, L, H, d, _DTYPES[q.dtype], *tensors, kind, eps, pairing, A, freq_ptr, axis_ptr, *where)
+        args = _ROPE_ARGS.pack(B, L, H, d, _DTYPES[q.dtype], *tensors, kind, eps, pairing, A, pairs[0], pairs[1], *where)
         rc = lib().sol_attn_rope(args, _raw_stream(dev))
         if rc:
             _check(rc)
-    return tuple(outs)
+    return outs
 
 
 # ------------------------------------------------------------------ products of 8-bit integers
