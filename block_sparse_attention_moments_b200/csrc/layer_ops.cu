@@ -341,7 +341,7 @@ int launch_linear_few(LinearParams p, const LinearOperands& o, int dev, int sms,
   const int split = 1 << log_split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * split);
-  cfg.blockDim = dim3(kLinThreads);
+  cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

@@ -7,7 +7,7 @@
 // linear_kernel: persistent, warp-specialised.  A pair of CTAs (cta_group::2)
 // works on a tile of 256 tokens x BN channels, a single CTA (cta_group::1) on
 // 128 x BN.  Warp 0 copies A and W tiles of 128 bytes of K by TMA into a ring
-// of stages, warp 1 issues the MMAs, warps 2-5 read the accumulators from TMEM
+// of stages, warp 1 issues the MMAs, warps 2-9 read the accumulators from TMEM
 // and write the output; two accumulators alternate, so that one tile's output
 // is written while the next one's products run.
 #pragma once
@@ -17,7 +17,8 @@
 
 namespace solattn {
 
-constexpr int kLinThreads = 192;
+constexpr int kLinThreads = 320;    // copies, MMAs, and eight warps for the output
+constexpr int kFewThreads = 192;
 constexpr int kLinStageA = 128 * 128;                    // bytes of A of a stage (of a CTA)
 constexpr uint64_t kLinTimeoutNs = 2000000000ull;
 
@@ -40,7 +41,7 @@ template <int CG, int BN>
 struct LinearConfig {
   static constexpr int kStageB = BN / CG * 128;
   static constexpr int kStage = kLinStageA + kStageB;
-  static constexpr int kOut = 4 * 2 * 4096;              // per epilogue warp two buffers of 32 rows x 128 bytes
+  static constexpr int kOut = 8 * 4096;                  // per output warp 32 rows x 128 bytes
   static constexpr int kStages = (224 * 1024 - kOut) / kStage > 8 ? 8 : (224 * 1024 - kOut) / kStage;
   static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int kParams = BN * 8;                 // the tile's scales and biases, fp32
@@ -160,10 +161,10 @@ __device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int* m
   *m = b * p.band + (r - *n * rows);
 }
 
-// Barrier 1 of the four epilogue warps; whether all of their threads are well.
+// Barrier 1 of the eight output warps; whether all of their threads are well.
 __device__ __forceinline__ bool all_of_epilogue(bool ok) {
   uint32_t r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                : "=r"(r)
                : "r"(static_cast<uint32_t>(ok))
                : "memory");
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4 * CG);   // the epilogue warps of the tile's CTAs
+      mbar_init(&acc_empty[i], 8 * CG);   // the output warps of the tile's CTAs
     }
     *abort = 0;
     fence_mbar_init();
@@ -251,10 +252,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (ok) umma_commit_all<CG>(&acc_full[buf]);
     }
   } else if (warp >= 2) {
-    const int q = warp & 3;                 // the TMEM lanes that this warp may read
-    uint8_t* stage_out = out_buf + q * 2 * 4096;
+    // Two warps to each quarter of the TMEM lanes (a warp may read the quarter
+    // of its number), every other chunk of columns each: one warp's conversions
+    // and stores fill the other's waits.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* sbuf = out_buf + (warp - 2) * 4096;
     constexpr int kCols = 128 / sizeof(T);  // channels of a 128-byte row of the output buffer
-    int tile = 0, chunk = 0;
+    int tile = 0;
     for (int t = first; t < tiles; t += step, ++tile) {
       int tm, tn;
       linear_tile(p, t, &tm, &tn);
@@ -263,40 +267,35 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int row = row0 + lane;
       const float sa = row < p.M ? p.a_scale[row] : 0.f;
       // the channels' scales and biases, fetched while the tile is being multiplied
-      float mine[2][BN / 128 > 0 ? BN / 128 : 1];
-#pragma unroll
-      for (int i = 0; i < (BN + 127) / 128; ++i) {
-        const int n = tn * BN + i * 128 + q * 32 + lane;
-        const bool there = i * 128 + q * 32 + lane < BN && n < p.N;
-        mine[0][i] = there ? p.w_scale[n] : 0.f;
-        mine[1][i] = there ? bias_at(p, n) : 0.f;
-      }
+      const int c = threadIdx.x - 64;
+      const bool there = c < BN && tn * BN + c < p.N;
+      const float scale = there ? p.w_scale[tn * BN + c] : 0.f, bias = there ? bias_at(p, tn * BN + c) : 0.f;
       // Those of the tile before have been read.  A warp whose wait gave up
-      // says so here, where the four leave together: none is left at a barrier.
+      // says so here, where all leave together: none is left at a barrier.
       ok = all_of_epilogue(ok);
       if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < (BN + 127) / 128; ++i) {
-        const int c = i * 128 + q * 32 + lane;
-        if (c < BN) params[c] = mine[0][i], params[BN + c] = mine[1][i];
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (c < BN) params[c] = scale, params[BN + c] = bias;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       ok = mbar_wait(&acc_full[buf], (tile >> 1) & 1, abort, kLinTimeoutNs);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) continue;
       tc_fence_after();
       const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
-      for (int c0 = 0; c0 < BN; c0 += kCols) {
+      // the last chunk of this warp (of narrow tiles the second warp has none)
+      const int last = BN - kCols >= half * kCols ? (BN / kCols - 1 - half) / 2 * 2 * kCols + half * kCols : -1;
+      if (last < 0 && lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[buf]), 0));
+        else mbar_arrive(&acc_empty[buf]);
+      }
+      for (int c0 = half * kCols; c0 < BN; c0 += 2 * kCols) {
         const int col0 = tn * BN + c0;
-        const bool last = c0 + kCols >= BN;
-        uint8_t* sbuf = stage_out + (chunk & 1) * 4096;
         uint32_t r[kCols];
 #pragma unroll
         for (int j = 0; j < kCols; j += 32) tmem_ld_x32f(src + c0 + j, reinterpret_cast<float*>(r) + j);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < kCols; j += 32) reg_fence32(reinterpret_cast<float*>(r) + j);
-        if (last) {   // the accumulator has been read
+        if (c0 == last) {   // this warp has read its part of the accumulator
           tc_fence_before();
           if (lane == 0) {
             if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[buf]), 0));
@@ -304,10 +303,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
         if (col0 >= p.N || row0 >= p.M) continue;
-        ++chunk;
-        // the TMA store of this buffer two chunks ago has read it
+        // the store of the chunk before has read the buffer
         if (!p.direct) {
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
         __syncwarp();
 #pragma unroll
@@ -477,7 +475,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
 }
 
 template <int BT, typename T>
-__global__ void __launch_bounds__(kLinThreads)
+__global__ void __launch_bounds__(kFewThreads)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ LinearParams p, int log_split) {
   using C = FewConfig<BT>;
@@ -507,7 +505,7 @@ __global__ void __launch_bounds__(kLinThreads)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_all<1>(tmem_slot, kTmem);
-  for (int i = threadIdx.x; i < BT; i += kLinThreads) a_scale[i] = i < tokens ? p.a_scale[t0 + i] : 0.f;
+  for (int i = threadIdx.x; i < BT; i += kFewThreads) a_scale[i] = i < tokens ? p.a_scale[t0 + i] : 0.f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
