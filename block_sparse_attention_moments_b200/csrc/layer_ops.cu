@@ -21,7 +21,10 @@ namespace {
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
 constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
-constexpr int kFewTokens = 128;                   // tokens up to which their tiles of 64 are taken
+// Tokens up to which channels are the rows of the tile (15360 x 5120: 128 tokens
+// in tiles of 64 23 us, in one tile of 128 rows 37; 5120 x 5120: 200 tokens 19
+// against 16.6 the other way round).
+constexpr int kFewTokens = 128;
 constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
 constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
 // Rows of a team at a time: two share the factors' reads and the barriers; of
@@ -362,20 +365,18 @@ int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms,
   if (p.M <= 16) return launch_linear_few<16, T>(p, o, dev, sms, st);
   if (p.M <= 32) return launch_linear_few<32, T>(p, o, dev, sms, st);
   if (p.M <= kFewTokens) return launch_linear_few<64, T>(p, o, dev, sms, st);
-  // The variant whose slowest SM is done first: waves of tiles, each the MMA
-  // time of its K (in units of 128 x 128 x 128 of an SM) and the time until
-  // the pipeline is full and the last output is written.
+  // The variant whose slowest SM is done first: waves of tiles, each the time
+  // of its K and of its output.  A block of 128 of K takes both variants the
+  // same 0.35 us, in which an SM is brought its 32 KB; the pair's tile is twice
+  // as wide.  5120 channels of 5120 (us, pair / single): 200 tokens 17.9 / 16.9,
+  // 512 18.6 / 28.6, 1024 32 / 41; 1034 x 1543 x 1000 14.6 / 10.0.
   const auto cost = [&](int cg, int bn) {
     const long long tiles = ((p.M + 128LL * cg - 1) / (128 * cg)) * ((p.N + bn - 1LL) / bn);
     const long long waves = (tiles + sms / cg - 1) / (sms / cg);
-    const int kblocks = (p.K + 127) / 128;
-    const double block = cg == 2 ? 2.0 : bn == 128 ? 1.5 : 1.0;
-    return waves * (kblocks * block + bn / 64.0) + 8.0;
+    return waves * ((p.K + 127) / 128 + bn / 64);
   };
-  const double c2 = cost(2, 256), c1 = cost(1, 128), ch = cost(1, 64);
-  if (c2 <= c1 && c2 <= ch) return launch_linear<2, 256, T>(p, o, dev, sms, st);
-  if (c1 <= ch) return launch_linear<1, 128, T>(p, o, dev, sms, st);
-  return launch_linear<1, 64, T>(p, o, dev, sms, st);
+  if (cost(2, 256) <= cost(1, 128)) return launch_linear<2, 256, T>(p, o, dev, sms, st);
+  return launch_linear<1, 128, T>(p, o, dev, sms, st);
 }
 
 }  // namespace
