@@ -27,10 +27,6 @@ constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring ke
 constexpr int kFewTokens = 128;
 constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
 constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
-// Rows of a team at a time: two share the factors' reads and the barriers; of
-// an fp32 stream and a block's output two do not leave room for enough teams.
-template <typename TX, bool RES>
-constexpr int kNormRingRows = RES && sizeof(TX) == 4 ? 1 : 2;
 constexpr size_t kRopeShared = 220 * 1024;       // shared memory of the rotary kernel
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
@@ -136,12 +132,12 @@ int launch_norm_as(NormParams p, int sms, cudaStream_t st) {
 }
 
 // Whether the call is one for the ring kernel; if it is, *rc is its status.
-template <typename TX, typename TY, bool RES, bool FULL, int WARPS>
+template <typename TX, typename TY, int R, bool RES, bool FULL, int WARPS>
 int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_t st) {
-  constexpr int R = kNormRingRows<TX, RES>, N = kNormRingVectors;
+  constexpr int N = kNormRingVectors;
   const int teams = p.warps > 1 ? std::min(15, kNormRingThreads / 32 / p.warps) : kNormRingThreads / 32;
-  const size_t row = static_cast<size_t>(p.warps) * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-  const int fit = R == 1 ? teams : static_cast<int>((kNormRingShared - factors) / (R * row));   // stages of all teams
+  const size_t stage = R == 1 ? 0 : static_cast<size_t>(p.warps) * R * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
+  const int fit = R == 1 ? teams : static_cast<int>((kNormRingShared - factors) / stage);   // stages of all teams
   const int used = std::min(teams, fit);
   p.depth = R == 1 ? 1 : std::min(4, fit / used);
   static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
@@ -150,39 +146,40 @@ int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormRingShared)));
     attr_set[dev] = true;
   }
-  norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>
-      <<<sms, used * p.warps * 32, factors + (R == 1 ? 0 : static_cast<size_t>(used) * p.depth * R * row), st>>>(p);
+  norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS><<<sms, used * p.warps * 32, factors + used * p.depth * stage, st>>>(p);
   CUDA_TRY(cudaGetLastError());
   return SOL_ATTN_OK;
 }
 
-// Whether the ring kernel takes the call: many rows of long groups, vectors of
-// 8, and factors that leave room for two teams' rows.
-template <typename TX, typename TY, bool RES>
-bool for_norm_ring(NormParams& p, size_t* factors, int sms) {
-  const long long rows = static_cast<long long>(p.B) * p.L;
-  const int per_warp = 32 * kNormRingVectors * 8;
-  p.warps = (p.C + per_warp - 1) / per_warp;
-  *factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
-  const size_t row = static_cast<size_t>(p.warps) * kNormRingVectors * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-  for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
-  return rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
-         (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift) &&
-         *factors + (kNormRingRows<TX, RES> == 1 ? 0 : 4 * row) <= kNormRingShared;
+template <typename TX, typename TY, int R, bool RES, bool FULL>
+int launch_norm_warps(const NormParams& p, size_t factors, int dev, int sms, cudaStream_t st) {
+  return p.warps == 1 ? launch_norm_ring<TX, TY, R, RES, FULL, 1>(p, factors, dev, sms, st)
+                      : launch_norm_ring<TX, TY, R, RES, FULL, 8>(p, factors, dev, sms, st);
 }
 
 template <typename TX, typename TY, bool RES>
-int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
+int launch_norm(NormParams p, bool vec, bool wide, int dev, int sms, cudaStream_t st) {
   if (vec) {
-    NormParams r = p;
-    size_t factors;
-    if (for_norm_ring<TX, TY, RES>(r, &factors, sms)) {
-      const bool full = p.C % (32 * kNormRingVectors * 8) == 0;
-      if (r.warps == 1)
-        return full ? launch_norm_ring<TX, TY, RES, true, 1>(r, factors, dev, sms, st)
-                    : launch_norm_ring<TX, TY, RES, false, 1>(r, factors, dev, sms, st);
-      return full ? launch_norm_ring<TX, TY, RES, true, 8>(r, factors, dev, sms, st)
-                  : launch_norm_ring<TX, TY, RES, false, 8>(r, factors, dev, sms, st);
+    // many rows of long groups, whose factors leave room for two teams' rows
+    const long long rows = static_cast<long long>(p.B) * p.L;
+    const int per_warp = 32 * kNormRingVectors * 8;
+    const size_t factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
+    p.warps = (p.C + per_warp - 1) / per_warp;
+    for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
+    if (rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
+        (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift)) {
+      const bool full = p.C % per_warp == 0;
+      if constexpr (sizeof(TX) == 4) {
+        if (factors <= kNormRingShared)
+          return full ? launch_norm_warps<TX, TY, 1, RES, true>(p, factors, dev, sms, st)
+                      : launch_norm_warps<TX, TY, 1, RES, false>(p, factors, dev, sms, st);
+      } else {
+        const size_t stage = static_cast<size_t>(p.warps) * 2 * kNormRingVectors * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
+        if (full && wide && factors <= kNormRingShared)
+          return launch_norm_warps<TX, TY, 1, RES, true>(p, factors, dev, sms, st);
+        if (factors + 2 * stage <= kNormRingShared)
+          return launch_norm_warps<TX, TY, 2, RES, false>(p, factors, dev, sms, st);
+      }
     }
     if (p.C <= 2816) return launch_norm_as<TX, TY, 8, 1, RES, 352>(p, sms, st);
     if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
@@ -195,8 +192,8 @@ int launch_norm(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st
 }
 
 template <typename TX, typename TY>
-int launch_norm_res(const NormParams& p, bool vec, int dev, int sms, cudaStream_t st) {
-  return p.y ? launch_norm<TX, TY, true>(p, vec, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, dev, sms, st);
+int launch_norm_res(const NormParams& p, bool vec, bool wide, int dev, int sms, cudaStream_t st) {
+  return p.y ? launch_norm<TX, TY, true>(p, vec, wide, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, wide, dev, sms, st);
 }
 
 template <typename T, bool HALF, int WARPS>
@@ -477,14 +474,18 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   p.pre = a->norm, p.post = a->post_norm;
   p.pre_eps = a->eps, p.post_eps = a->post_eps;
 
+  // whether 32-byte vectors can read and write the rows of a 16-bit type
+  const bool wide = p.x_inner % 16 == 0 && aligned(32, p.x, xs, {p.x_sb, p.x_sl, p.x_sh}) && aligned(32, p.y, ys, {p.y_sb, p.y_sl}) &&
+                    aligned(32, p.xo, xs, {p.xo_sb, p.xo_sl}) && aligned(32, p.h, ys, {p.h_sb, p.h_sl}) &&
+                    aligned(16, p.q, 1, {p.q_sl});
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, dev, sms, st);
-  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, dev, sms, st);
-  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, dev, sms, st);
-  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, dev, sms, st);
-  return launch_norm_res<float, float>(p, vec, dev, sms, st);
+  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, wide, dev, sms, st);
+  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, wide, dev, sms, st);
+  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, wide, dev, sms, st);
+  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, wide, dev, sms, st);
+  return launch_norm_res<float, float>(p, vec, wide, dev, sms, st);
 }
 
 int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {

@@ -172,11 +172,32 @@ __device__ __forceinline__ void normalise(Team& t, int kind, float eps, const No
   }
 }
 
+template <int V, int N, bool WIDE, typename T>
+__device__ __forceinline__ void store_vectors(T* p, const bool (&on)[N], const float (&v)[N][V]) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      uint4 u[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u[h] = make_uint4(narrow2<T>(v[i + h][0], v[i + h][1]), narrow2<T>(v[i + h][2], v[i + h][3]),
+                          narrow2<T>(v[i + h][4], v[i + h][5]), narrow2<T>(v[i + h][6], v[i + h][7]));
+      st_row_v8(p + i * 32 * V, u[0], u[1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) store_row(p + i * 32 * V, v[i]);
+  }
+}
+
 // What happens to R rows v = x' (unrounded) of a team, tokens l, l + 1 of batch
 // element b, of which those with `keep` are its: x' is written, normed,
 // modulated with the factors that pre(i, a, c) gives, and written as h and in
 // 8 bits.
-template <typename TX, typename TY, int R, int V, int N, bool RES, class Team, class Pre>
+// A thread's vectors are first, first + 32, ...; WIDE: pairs of neighbours,
+// first, first + 1, first + 64, first + 65, ..., stored as one.
+template <typename TX, typename TY, int R, int V, int N, bool RES, bool WIDE, class Team, class Pre>
 __device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsigned row, int b, int l, int first,
                                           const bool (&keep)[R], const bool (&on)[N], float (&v)[R][N][V], Pre pre) {
   if constexpr (RES) {
@@ -185,9 +206,7 @@ __device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsig
       for (int r = 0; r < R; ++r) {
         if (!keep[r]) continue;
         TX* op = static_cast<TX*>(p.xo) + b * p.xo_sb + (l + r) * p.xo_sl + first * V;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (on[i]) store_row(op + i * 32 * V, v[r][i]);
+        store_vectors<V, N, WIDE>(op, on, v[r]);
       }
     }
     if (!p.h && !p.q) return;
@@ -206,9 +225,7 @@ __device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsig
     for (int r = 0; r < R; ++r) {
       if (!keep[r]) continue;
       TY* hp = static_cast<TY*>(p.h) + b * p.h_sb + (l + r) * p.h_sl + first * V;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (on[i]) store_row(hp + i * 32 * V, v[r][i]);
+      store_vectors<V, N, WIDE>(hp, on, v[r]);
     }
   }
   if (p.q) {
@@ -243,9 +260,17 @@ __device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsig
           for (int j = 0; j < V; ++j) v[r][i][j] = tiny ? v[r][i][j] * 0x1p100f : 0.f;
       }
       int8_t* qp = p.q + (row + r) * p.q_sl + first * V;
+      if constexpr (WIDE) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (on[i]) store_s8<V>(qp + i * 32 * V, v[r][i], up);
+        for (int i = 0; i < N; i += 2) {
+          const uint2 a = pack_s8(v[r][i], up), c = pack_s8(v[r][i + 1], up);
+          *reinterpret_cast<uint4*>(qp + i * 32 * V) = make_uint4(a.x, a.y, c.x, c.y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (on[i]) store_s8<V>(qp + i * 32 * V, v[r][i], up);
+      }
       if (first == 0) p.q_scale[row + r] = amax[r] / 127.f;
     }
   }
@@ -340,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 352 ? 2 : 1) norm_kernel(c
     }
     if (row + 1 < end) load(row + 1);
     const bool keep[1] = {true};
-    emit_rows<TX, TY, 1, V, N, RES>(p, team, row, b, l, first, keep, on, v, [&](int i, float(&a)[V], float(&c)[V]) {
+    emit_rows<TX, TY, 1, V, N, RES, false>(p, team, row, b, l, first, keep, on, v, [&](int i, float(&a)[V], float(&c)[V]) {
 #pragma unroll
       for (int j = 0; j < V; ++j) a[j] = A[i][j], c[j] = Bv[i][j];
     });
@@ -349,21 +374,24 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 352 ? 2 : 1) norm_kernel(c
 
 // Many rows of long groups.  The block folds the factors of a group into
 // shared memory and its teams, each with every teams-th R rows of the block's
-// share, read them from there, once for R rows.  With R = 2 the rows come
-// through a ring of p.depth stages of R rows in shared memory by asynchronous
-// copies, each warp's part by that warp: rows on their way cost no registers,
-// and no barrier but the warp's own.  With R = 1 (an fp32 stream and a block's
-// output, whose factors leave little room) the next row is on its way in
-// registers: 75600 x 5120, fp32 and bf16, takes 737 us so and 830 through the
-// ring; the bf16 norm alone takes 362 us in registers and 288 through the ring.
+// share, read them from there, once for R rows.
+// R = 1: a thread's vectors are 32 bytes (8 of fp32, or two neighbours of 8 of
+// a 16-bit type: WIDE), and the next row is on its way in registers.  R = 2,
+// for 16-bit rows that 32-byte vectors do not fill: 16 bytes a vector, and the
+// rows come through a ring of p.depth stages of R rows in shared memory by
+// asynchronous copies, each warp's part by that warp.  75600 x 5120:
+//   fp32 to 8 bits           R = 1 305 us, R = 2 through the ring 454
+//   fp32 with bf16 output    R = 1 737 us, ring 830
+//   bf16                     R = 1 KWIDE us with 32-byte vectors, 362 with 16, ring 287
 // FULL: the teams' threads have exactly the row's vectors.  R rows that a
 // group's end divides are taken twice, once with each group's factors, and
 // each of them is kept once.
-// (R = 1 only with RES.)
 template <typename TX, typename TY, int R, int N, bool RES, bool FULL, int WARPS>
 __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormParams p) {
   constexpr int V = 8;
   constexpr int kX = N * 32 * V * sizeof(TX), kY = RES ? N * 32 * V * sizeof(TY) : 0;   // bytes of a warp's row
+  constexpr bool WIDE = R == 1 && sizeof(TX) == 2;
+  static_assert(!WIDE || FULL, "pairs of vectors fill the row");
   constexpr bool RING = R > 1;
   constexpr int kStage = R * (kX + kY);
   using TeamR = Team<WARPS, R>;
@@ -374,8 +402,12 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
   team.make(p.warps, slots, kTeamSlots);
   const int lane = threadIdx.x % 32;
   const int teams = blockDim.x / 32 / team.warps;
-  const int first = team.warp * 32 * N + lane;
+  const int first = team.warp * 32 * N + (WIDE ? 2 : 1) * lane;
   const int nvec = p.C / V;
+  // where a vector's factors lie (WIDE: even vectors, then odd ones, as lanes read every other one)
+  auto place = [&](int vec) { return WIDE ? (vec >> 1) + (vec & 1 ? nvec >> 1 : 0) : vec; };
+  const int mine = WIDE ? (team.warp * 32 * N >> 1) + lane : first;
+  auto factor = [&](int i) { return WIDE ? mine + (i >> 1) * 32 + (i & 1 ? nvec >> 1 : 0) : mine + i * 32; };
   const unsigned L = p.L, rows = p.B * L;   // below 2^31
   const int planes = RES ? (p.post_bias.p ? 4 : 3) : 2;
   uint8_t* ring = reinterpret_cast<uint8_t*>(factors + planes * p.C) + (threadIdx.x / 32) * p.depth * kStage;
@@ -395,16 +427,32 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     nl += R * teams;
     while (nl >= p.L && next < end) nl -= p.L, ++nb;
   };
-  Raw<TX, V> rx[RING ? 1 : N];   // without a ring: the row on its way
-  Raw<TY, V> ry[RING ? 1 : N];
+  Raw<TX, V> rx[RING ? 1 : N];          // without a ring: the row on its way
+  Raw<TY, V> ry[RING || !RES ? 1 : N];
   auto load = [&](int stage) {
     if constexpr (!RING) {
       if (next < end) {
-        const TX* xp = static_cast<const TX*>(p.x) + nb * p.x_sb + nl * p.x_sl + first * V;
+        const TX* xp = static_cast<const TX*>(p.x) + nb * p.x_sb + nl * p.x_sl;
         const TY* yp = static_cast<const TY*>(p.y) + nb * p.y_sb + nl * p.y_sl + first * V;
+        auto piece = [&](int c) {   // channel c of a row of pieces
+          return xp + (c >> p.inner_shift) * p.x_sh + (c & ((1 << p.inner_shift) - 1));
+        };
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (on[i]) load_raw(rx[i], xp + i * 32 * V), load_raw(ry[i], yp + i * 32 * V);
+          for (int i = 0; i < N; i += 2) {
+            const int c = (first + i * 32) * V;
+            ld_row_v8(p.x_inner == p.C ? xp + c : piece(c), rx[i].r[0], rx[i + 1].r[0]);
+            if constexpr (RES) ld_row_v8(yp + i * 32 * V, ry[i].r[0], ry[i + 1].r[0]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (!on[i]) continue;
+            const int c = (first + i * 32) * V;
+            load_raw(rx[i], p.x_inner == p.C ? xp + c : piece(c));
+            if constexpr (RES) load_raw(ry[i], yp + i * 32 * V);
+          }
+        }
       }
       advance();
       return cp_async_commit();
@@ -462,12 +510,12 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     for (int vec = threadIdx.x; vec < nvec; vec += blockDim.x) {
       float a[1][V], c[1][V];
       fold_pre<V, 1>(p, b, l0, vec * V, 0, a, c);
-      put_factor<V>(factors, nvec, vec, a[0]);
-      put_factor<V>(factors + p.C, nvec, vec, c[0]);
+      put_factor<V>(factors, nvec, place(vec), a[0]);
+      put_factor<V>(factors + p.C, nvec, place(vec), c[0]);
       if constexpr (RES) {
         fold_post<V, 1>(p, b, l0, vec * V, 0, a, c);
-        put_factor<V>(factors + 2 * p.C, nvec, vec, a[0]);
-        if (p.post_bias.p) put_factor<V>(factors + 3 * p.C, nvec, vec, c[0]);
+        put_factor<V>(factors + 2 * p.C, nvec, place(vec), a[0]);
+        if (p.post_bias.p) put_factor<V>(factors + 3 * p.C, nvec, place(vec), c[0]);
       }
     }
     __syncthreads();
@@ -490,7 +538,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           if (on[i]) {
-            if constexpr (!RING) widen(ry[i], v[r][i]);
+            if constexpr (!RING && RES) widen(ry[i], v[r][i]);
+            else if constexpr (!RING) widen(rx[i], v[r][i]);
             else if constexpr (RES) take_staged<TY>(src + r * (kX + kY) + kX, i * 32 + lane, v[r][i]);
             else take_staged<TX>(src + r * (kX + kY), i * 32 + lane, v[r][i]);
           } else {
@@ -505,8 +554,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
         for (int i = 0; i < N; ++i) {
           if (!on[i]) continue;
           float a[V], c[V];
-          get_factor<V>(factors + 2 * p.C, nvec, first + i * 32, a);
-          if (p.post_bias.p) get_factor<V>(factors + 3 * p.C, nvec, first + i * 32, c);
+          get_factor<V>(factors + 2 * p.C, nvec, factor(i), a);
+          if (p.post_bias.p) get_factor<V>(factors + 3 * p.C, nvec, factor(i), c);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             float x[V];
@@ -526,10 +575,10 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
         stage = stage + 1 == p.depth ? 0 : stage + 1;
         row += R * teams;
       }
-      emit_rows<TX, TY, R, V, N, RES>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
+      emit_rows<TX, TY, R, V, N, RES, WIDE>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
                                       [&](int i, float(&a)[V], float(&c)[V]) {
-                                        get_factor<V>(factors, nvec, first + i * 32, a);
-                                        get_factor<V>(factors + p.C, nvec, first + i * 32, c);
+                                        get_factor<V>(factors, nvec, factor(i), a);
+                                        get_factor<V>(factors + p.C, nvec, factor(i), c);
                                       });
       if (again) break;
     }

@@ -249,26 +249,24 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   return r;
 }
 
-// V values times `up`, to the nearest whole numbers (ties to even), as s8, the
+// Values times `up`, to the nearest whole numbers (ties to even), as s8, the
 // first in the lowest byte.  |v * up| <= 127: adding 1.5 * 2^23 leaves the
 // whole number in the low bits of the sum, rounded once.
+__device__ __forceinline__ uint2 pack_s8(const float (&v)[8], float up) {
+  const float2 u = make_float2(up, up), magic = make_float2(12582912.f, 12582912.f);
+  uint32_t k[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), u, magic);
+    k[j] = __float_as_uint(r.x), k[j + 1] = __float_as_uint(r.y);
+  }
+  return make_uint2(__byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(k[4], k[5], 0x0040), __byte_perm(k[6], k[7], 0x0040), 0x5410));
+}
 template <int V>
 __device__ __forceinline__ void store_s8(int8_t* p, const float (&v)[V], float up) {
-  if constexpr (V == 8) {
-    const float2 u = make_float2(up, up), magic = make_float2(12582912.f, 12582912.f);
-    uint32_t k[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), u, magic);
-      k[j] = __float_as_uint(r.x), k[j + 1] = __float_as_uint(r.y);
-    }
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(__byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410),
-                   __byte_perm(__byte_perm(k[4], k[5], 0x0040), __byte_perm(k[6], k[7], 0x0040), 0x5410));
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = static_cast<int8_t>(__float_as_uint(fmaf(v[j], up, 12582912.f)));
-  }
+  if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = pack_s8(v, up);
+  else *p = static_cast<int8_t>(__float_as_uint(fmaf(v[0], up, 12582912.f)));
 }
 
 // N vectors of V consecutive parameters, `step` elements apart, whose type is

@@ -472,3 +472,25 @@ def test_offsets_past_32_bits():
     out = big.as_strided((2, L, C), (2 ** 31 + 16, 64, 1), 8)
     sa.norm_modulate(v, out=out)
     assert torch.equal(out, sa.norm_modulate(v)) and torch.equal(x, v)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [1024, 5120])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_many_rows_at_any_alignment(C, dtype):
+    """Rows at multiples of 32, 16 and 2 bytes, in and out, and groups that end at odd rows: the same values."""
+    B, G, per = 2, 3, 1601
+    L = G * per
+    x, y = randn(B, L, C, dtype=dtype), randn(B, L, C, dtype=dtype)
+    scale = randn(B, G, C, std=0.3)
+    want_x, size_x, want, size = reference(x, y, None, scale, scale)
+    for off in (0, 16, 8, 4, 1):
+        a, b = (torch.zeros(B, L, C + 16, device="cuda", dtype=dtype)[..., off:off + C] for _ in range(2))
+        a.copy_(x), b.copy_(y)
+        out, x_out = (torch.full((B, L, C + 16), 3.0, device="cuda", dtype=dtype) for _ in range(2))
+        sa.gate_residual_norm(a, b, None, scale, scale, x_out=x_out[..., off:off + C], out=out[..., off:off + C])
+        close(x_out[..., off:off + C], want_x, size_x, f"x' at {off}")
+        close(out[..., off:off + C], want, size, f"h at {off}")
+        assert (out[..., :off] == 3).all() and (out[..., off + C:] == 3).all()
+        q, s = sa.quantize_rows(a)
+        check_quantised(q, s, x.double(), torch.zeros_like(x, dtype=torch.float64))
