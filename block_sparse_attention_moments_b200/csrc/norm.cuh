@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 352 ? 2 : 1) norm_kernel(c
 // asynchronous copies, each warp's part by that warp.  75600 x 5120:
 //   fp32 to 8 bits           R = 1 305 us, R = 2 through the ring 454
 //   fp32 with bf16 output    R = 1 737 us, ring 830
-//   bf16                     R = 1 KWIDE us with 32-byte vectors, 362 with 16, ring 287
+//   bf16                     R = 1 266 us with 32-byte vectors, 362 with 16, ring 287
 // FULL: the teams' threads have exactly the row's vectors.  R rows that a
 // group's end divides are taken twice, once with each group's factors, and
 // each of them is kept once.
@@ -527,7 +527,12 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
       else if (p.depth == 2) cp_async_wait<1>();
       else if (p.depth == 3) cp_async_wait<2>();
       else cp_async_wait<3>();
-      __syncwarp();
+      // A team that begins a row together reads and writes in longer runs: with
+      // a block's output, 75600 x 5120 bf16 533 us without this meeting and 490
+      // with it, fp32 without a norm 636 and 607; an fp32 stream with a norm
+      // behind it (739 without, 791 with) and lone norms (270, 280) do without.
+      if (RES && (WIDE || (!p.h && !p.q))) team.sync();
+      else __syncwarp();
       [[maybe_unused]] const uint8_t* src = ring + stage * kStage;
       bool keep[R];
 #pragma unroll
