@@ -131,7 +131,6 @@ int launch_norm_as(NormParams p, int sms, cudaStream_t st) {
   return SOL_ATTN_OK;
 }
 
-// Whether the call is one for the ring kernel; if it is, *rc is its status.
 template <typename TX, typename TY, int R, bool RES, bool FULL, int WARPS>
 int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_t st) {
   constexpr int N = kNormRingVectors;
@@ -183,6 +182,7 @@ int launch_norm(NormParams p, bool vec, bool wide, int dev, int sms, cudaStream_
     }
     if (p.C <= 2816) return launch_norm_as<TX, TY, 8, 1, RES, 352>(p, sms, st);
     if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
+    if (p.C <= 8192) return launch_norm_as<TX, TY, 8, 2, RES, 512>(p, sms, st);
     return launch_norm_as<TX, TY, 8, 4, RES, 512>(p, sms, st);
   }
   if (p.C <= 1408) return launch_norm_as<TX, TY, 1, 4, RES, 352>(p, sms, st);
@@ -466,6 +466,13 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
       (rc = convert(a->post_weight, "post_weight", B, L, &p.post_weight, &vec)) ||
       (rc = convert(a->post_bias, "post_bias", B, L, &p.post_bias, &vec)))
     return rc;
+  const sol_attn_vectors* vectors[7] = {&a->scale, &a->shift, &a->gate, &a->weight, &a->bias, &a->post_weight, &a->post_bias};
+  for (const sol_attn_vectors* v : vectors) {
+    if (!v->data) continue;
+    const Span s = span(v->data, dtype_size(v->dtype), v->stride_b, v->stride_g, B, v->groups, C);
+    for (int i = 0; i < nouts; ++i)
+      if (overlap(outs[i], s)) return fail(SOL_ATTN_ERR_ARG, "an output overlaps a vector of parameters");
+  }
   p.group = L;
   for (const Vectors* v : {&p.scale, &p.shift, &p.gate})
     if (v->p) p.group = std::gcd(p.group, v->per);
@@ -521,7 +528,8 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
     if (a->pos_kind < SOL_ATTN_POS_GRID || a->pos_kind > SOL_ATTN_POS_F64)
       return fail(SOL_ATTN_ERR_ARG, "unknown kind of positions %d", a->pos_kind);
     p.pos = a->positions;
-    p.pos_sb = a->pos_stride_b, p.pos_sl = a->pos_stride_l, p.pos_sa = a->pos_stride_a;
+    p.pos_sb = B > 1 ? a->pos_stride_b : 0, p.pos_sl = L > 1 ? a->pos_stride_l : 0, p.pos_sa = a->axes > 1 ? a->pos_stride_a : 0;
+    if (p.pos_sb < 0 || p.pos_sl < 0 || p.pos_sa < 0) return fail(SOL_ATTN_ERR_ARG, "positions has a negative stride");
   }
   p.pos_kind = a->pos_kind;
   if (B == 0 || L == 0) return SOL_ATTN_OK;
@@ -576,6 +584,16 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
         return fail(SOL_ATTN_ERR_ARG, "two outputs overlap");
     }
   }
+  for (int i = 0; i < tensors; ++i) {
+    const Span o = span(out[i]->out, size, 0, 0, 1, 1, n);
+    for (int j = 0; j < 2; ++j)
+      if (out[j]->weight &&
+          overlap(o, span(out[j]->weight, dtype_size(out[j]->weight_dtype), 0, 0, 1, 1, p.norm == kRopeNormToken ? H * d : d)))
+        return fail(SOL_ATTN_ERR_ARG, "an output overlaps a weight");
+    if (p.pos && overlap(o, span(p.pos, p.pos_kind == kPosI32 || p.pos_kind == kPosF32 ? 4 : 8, 0, 0, 1, 1,
+                                 (B - 1) * p.pos_sb + (L - 1) * p.pos_sl + (a->axes - 1) * p.pos_sa + 1)))
+      return fail(SOL_ATTN_ERR_ARG, "an output overlaps the positions");
+  }
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
@@ -589,6 +607,8 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
   const int M = a->M, N = a->N, K = a->K;
   int rc;
   if (M < 0 || N < 0 || K < 1) return fail(SOL_ATTN_ERR_ARG, "bad sizes M = %d, N = %d, K = %d", M, N, K);
+  if (M > INT_MAX - 512 || N > INT_MAX - 512) return fail(SOL_ATTN_ERR_UNSUPPORTED, "M = %d or N = %d is too large", M, N);
+  if (a->flags & ~SOL_ATTN_FLAG_TEST_STALL) return fail(SOL_ATTN_ERR_ARG, "unknown flag bits 0x%x", a->flags);
   if (K > kMaxLinearK) return fail(SOL_ATTN_ERR_UNSUPPORTED, "K = %d exceeds %d, up to which the sums fit 32 bits", K, kMaxLinearK);
   if (!dtype_ok(a->out_dtype)) return fail(SOL_ATTN_ERR_ARG, "out: unknown dtype %d", a->out_dtype);
   if (M == 0 || N == 0) return SOL_ATTN_OK;
@@ -606,6 +626,8 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
   LinearParams p{};
   p.M = M, p.N = N, p.K = K;
   p.a_scale = a->a_scale, p.w_scale = a->w_scale;
+  p.stall = (a->flags & SOL_ATTN_FLAG_TEST_STALL) != 0;
+  p.timeout_ns = p.stall ? 1000000ull : 2000000000ull;
   if (a->bias) {
     if (!dtype_ok(a->bias_dtype)) return fail(SOL_ATTN_ERR_ARG, "bias: unknown dtype %d", a->bias_dtype);
     if (reinterpret_cast<uintptr_t>(a->bias) % dtype_size(a->bias_dtype))
@@ -640,7 +662,8 @@ int sol_attn_linear_status(void* stream) {
   if (!h) return SOL_ATTN_OK;
   const unsigned zero = 0;
   CUDA_TRY(cudaMemcpyToSymbol(g_linear_status, &zero, sizeof(zero)));
-  return fail(SOL_ATTN_ERR_TIMEOUT, "a bounded device wait of a product gave up (status 0x%x)", h);
+  if (h & 1u) return fail(SOL_ATTN_ERR_TIMEOUT, "a bounded device wait of a product gave up (status 0x%x)", h);
+  return fail(SOL_ATTN_ERR_DEVICE, "a product's shared memory is not aligned to its tiles (status 0x%x)", h);
 }
 
 }  // extern "C"

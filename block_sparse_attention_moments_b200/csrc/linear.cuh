@@ -20,10 +20,16 @@ namespace solattn {
 constexpr int kLinThreads = 320;    // copies, MMAs, and eight warps for the output
 constexpr int kFewThreads = 192;
 constexpr int kLinStageA = 128 * 128;                    // bytes of A of a stage (of a CTA)
-constexpr uint64_t kLinTimeoutNs = 2000000000ull;
 
-// Set by a kernel whose wait gave up; read by sol_attn_linear_status.
+// Set by a kernel whose wait gave up (1) or whose shared memory lies at another
+// alignment than the tiles' swizzle needs (2); read by sol_attn_linear_status.
 static __device__ unsigned g_linear_status;
+
+__device__ __forceinline__ bool tiles_aligned(const void* base) {
+  if ((smem_u32(base) & 1023) == 0) return true;
+  atomicOr(&g_linear_status, 2u);
+  return false;
+}
 
 struct LinearParams {
   int M, N, K;
@@ -35,6 +41,8 @@ struct LinearParams {
   void* out;
   long long out_pitch;          // elements
   int direct;                   // the output's rows are not aligned for TMA
+  int stall;                    // test of the waits' limits: nothing is copied
+  unsigned long long timeout_ns;
 };
 
 template <int CG, int BN>
@@ -177,6 +185,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
   using C = LinearConfig<CG, BN>;
   extern __shared__ __align__(1024) uint8_t base[];
+  if (!tiles_aligned(base)) return;
   uint8_t* out_buf = base + C::kStages * C::kStage;
   float* params = reinterpret_cast<float*>(out_buf + C::kOut);   // scales, then biases, of the tile's channels
   uint64_t* full = reinterpret_cast<uint64_t*>(params + 2 * BN);
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int kblocks = (p.K + 127) / 128;
   bool ok = true;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0 && !p.stall) {
     int it = 0;
     for (int t = first; t < tiles && ok; t += step) {
       int tm, tn;
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int row_w = tn * BN + rank * (BN / CG);
       for (int k = 0; k < kblocks; ++k, ++it) {
         const int s = it % C::kStages;
-        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort, kLinTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort, p.timeout_ns)) { ok = false; break; }
         if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::kStage);
         uint32_t bar = smem_u32(&full[s]);
         if constexpr (CG == 2) bar = map_to_rank(bar, 0);
@@ -235,12 +244,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int it = 0, tile = 0;
     for (int t = first; t < tiles && ok; t += step, ++tile) {
       const int buf = tile & 1;
-      if (!mbar_wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1, abort, kLinTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1, abort, p.timeout_ns)) { ok = false; break; }
       tc_fence_after();
       const uint32_t d = tmem + buf * BN;
       for (int k = 0; k < kblocks; ++k, ++it) {
         const int s = it % C::kStages;
-        if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort, kLinTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort, p.timeout_ns)) { ok = false; break; }
         tc_fence_after();
         const uint32_t sa = smem_u32(base + s * C::kStage);
         const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sa + kLinStageA, 16, 1024);
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) break;
       if (c < BN) params[c] = scale, params[BN + c] = bias;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      ok = mbar_wait(&acc_full[buf], (tile >> 1) & 1, abort, kLinTimeoutNs);
+      ok = mbar_wait(&acc_full[buf], (tile >> 1) & 1, abort, p.timeout_ns);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) continue;
       tc_fence_after();
@@ -480,6 +489,7 @@ __global__ void __launch_bounds__(kFewThreads)
                       const __grid_constant__ LinearParams p, int log_split) {
   using C = FewConfig<BT>;
   extern __shared__ __align__(1024) uint8_t base[];
+  if (!tiles_aligned(base)) return;
   uint32_t* parts = reinterpret_cast<uint32_t*>(base + C::kStages * C::kStage);   // [split][BT / split][128]
   float* a_scale = reinterpret_cast<float*>(parts + BT * 128);
   uint64_t* full = reinterpret_cast<uint64_t*>(a_scale + BT);
@@ -513,10 +523,10 @@ __global__ void __launch_bounds__(kFewThreads)
   const int kblocks = (p.K + 127) / 128;
   const int k0 = kblocks * rank / split, k1 = kblocks * (rank + 1) / split;   // never empty: split <= kblocks
   bool ok = true;
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0 && !p.stall) {
     for (int k = k0; k < k1; ++k) {
       const int it = k - k0, s = it % C::kStages;
-      if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort, kLinTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort, p.timeout_ns)) { ok = false; break; }
       mbar_arrive_expect_tx(&full[s], C::kStage);
       const uint32_t dst = smem_u32(base + s * C::kStage);
       tma_load_2d<1>(dst, &map_w, smem_u32(&full[s]), k * 128, n0);
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads)
     constexpr uint32_t idesc = idesc_s8_s32(128, BT);
     for (int k = k0; k < k1; ++k) {
       const int it = k - k0, s = it % C::kStages;
-      if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort, kLinTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort, p.timeout_ns)) { ok = false; break; }
       tc_fence_after();
       const uint32_t sw = smem_u32(base + s * C::kStage);
       const uint64_t dw = sdesc_sw128(sw, 16, 1024), da = sdesc_sw128(sw + kLinStageA, 16, 1024);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(kFewThreads)
   const float ws = warp >= 2 && n < p.N ? p.w_scale[n] : 0.f, b = warp >= 2 && n < p.N ? bias_at(p, n) : 0.f;
   uint32_t r[BT];
   if (warp >= 2) {
-    ok = mbar_wait(acc_full, 0, abort, kLinTimeoutNs);
+    ok = mbar_wait(acc_full, 0, abort, p.timeout_ns);
     ok = __all_sync(0xFFFFFFFFu, ok);
     tc_fence_after();
     if (ok) {
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(kFewThreads)
         st_cluster(map_to_rank(mine + (j & (each - 1)) * 512, j >> (31 - __clz(each))), r[j]);
     }
     cluster_sync();
-    if (warp >= 2 && n < p.N) {
+    if (warp >= 2 && ok && n < p.N) {
       const int m0 = rank * each, count = min(each, tokens - m0);
       T* o = static_cast<T*>(p.out) + (t0 + m0) * p.out_pitch + n;
 #pragma unroll 4
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(kFewThreads)
         o[j * p.out_pitch] = from_f32<T>(linear_value(sum, a_scale[m0 + j], ws, b));
       }
     }
-  } else if (warp >= 2 && n < p.N) {
+  } else if (warp >= 2 && ok && n < p.N) {
     T* o = static_cast<T*>(p.out) + t0 * p.out_pitch + n;
 #pragma unroll
     for (int j = 0; j < BT; ++j)

@@ -36,7 +36,7 @@ _POSITIONS = {torch.int32: 1, torch.int64: 2, torch.float32: 3, torch.float64: 4
 _ROWS, _VECTORS, _ROPE_TENSOR = "Piqq", "Piiqq", "PqqqPPi4x"
 _NORM_ARGS = struct.Struct("@iiiiq" + 4 * _ROWS + "PqPfifif" + 7 * _VECTORS)
 _ROPE_ARGS = struct.Struct("@iiiii" + 3 * _ROPE_TENSOR + "ifiiPPiiiiqPqqq")
-_LINEAR_ARGS = struct.Struct("@iiiPqPPqPPiPiq")
+_LINEAR_ARGS = struct.Struct("@iiiPqPPqPPiPiqI4x")
 _NO_ROWS, _NO_VECTORS = (0, 0, 0, 0), (0, 0, 0, 0, 0)
 _NO_AFFINE = _NO_VECTORS + _NO_VECTORS
 
@@ -429,7 +429,7 @@ def int8_linear(a, a_scale, w, w_scale, bias=None, *, out_dtype=None, out=None):
         b = (bias.data_ptr(), _DTYPES[bias.dtype])
     if M and N:
         args = _LINEAR_ARGS.pack(M, N, K, a.data_ptr(), pitch, a_scale.data_ptr(), w.data_ptr(), w_strides[0],
-                                 w_scale.data_ptr(), *b, out.data_ptr(), _DTYPES[out.dtype], N)
+                                 w_scale.data_ptr(), *b, out.data_ptr(), _DTYPES[out.dtype], N, 0)
         rc = lib().sol_attn_quantized_linear(args, _raw_stream(dev))
         if rc:
             _check(rc)

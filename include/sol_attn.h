@@ -268,7 +268,7 @@ typedef struct sol_attn_norm_args {
  * with norm(v) = (v - mean) / sqrt(var + eps) * weight + bias (layer),
  * v / sqrt(mean(v^2) + eps) * weight + bias (rms) or v * weight + bias (none).
  * Outputs, each where wanted: x', h, and h in 8 bits: q_scale = max|h| / 127 of
- * the row and q = h / q_scale to the nearest whole number, ties to even.  A row
+ * the row and q = h * (127 / max|h|) to the nearest whole number, ties to even.  A row
  * of zeros has the scale 0; a row that holds an infinity or a NaN has a scale
  * that is not finite and zeros for q. */
 int sol_attn_norm_modulate(const sol_attn_norm_args* args, void* stream);
@@ -332,6 +332,10 @@ typedef struct sol_attn_linear_args {
   void* out;                     /* [M, N], overlaps no input */
   int out_dtype;
   long long out_stride;
+  unsigned flags;                /* 0, or SOL_ATTN_FLAG_TEST_STALL: test of the failure path
+                                    only, from 5 tokens on: nothing is copied, every bounded
+                                    wait gives up after 1 ms, out is left unwritten and
+                                    sol_attn_linear_status reports SOL_ATTN_ERR_TIMEOUT */
 } sol_attn_linear_args;
 
 /* Product of 8-bit integers with a scale for each token and each channel:
@@ -341,7 +345,8 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* args, void* stream);
 
 /* Status of the products enqueued on this device: synchronises stream and
  * returns SOL_ATTN_OK, or SOL_ATTN_ERR_TIMEOUT (and clears the status) if a
- * bounded wait of one of them gave up, whose output is then not valid. */
+ * bounded wait of one of them gave up, whose output is then not valid, or
+ * SOL_ATTN_ERR_DEVICE if one refused to run. */
 int sol_attn_linear_status(void* stream);
 
 #ifdef __cplusplus

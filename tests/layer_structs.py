@@ -35,4 +35,4 @@ class RopeArgs(ctypes.Structure):
 class LinearArgs(ctypes.Structure):
     _fields_ = [("M", _i), ("N", _i), ("K", _i), ("a", _vp), ("a_stride", _ll), ("a_scale", _vp), ("w", _vp),
                 ("w_stride", _ll), ("w_scale", _vp), ("bias", _vp), ("bias_dtype", _i), ("out", _vp), ("out_dtype", _i),
-                ("out_stride", _ll)]
+                ("out_stride", _ll), ("flags", ctypes.c_uint)]

@@ -152,3 +152,39 @@ def test_packed_arguments_are_the_structs():
             for part in name.split("."):
                 x = getattr(x, part)
             assert x == value, name
+
+
+FIRST_CALLS = """
+import torch
+import block_sparse_attention_moments_b200 as sa
+x = torch.randn(2, 300, 512, device="cuda", dtype=torch.bfloat16)
+wide = torch.randn(1, 5000, 1024, device="cuda", dtype=torch.bfloat16)
+w = torch.randint(-127, 128, (1536, 512), device="cuda", dtype=torch.int8)
+ws = torch.rand(1536, device="cuda")
+static = [torch.zeros(n, 512, device="cuda", dtype=torch.int8) for n in (2, 40)]
+scales = [torch.ones(n, device="cuda") for n in (2, 40)]
+def calls():
+    q, s = sa.norm_modulate(x, quantize=True)
+    qkv = sa.int8_linear(q, s, w, ws).view(2, 300, 3, 4, 128)
+    return (*sa.rope(*qkv.unbind(2), grid=(3, 10, 10), norm="token"), *sa.gate_residual_norm(wide, wide),
+            *(sa.int8_linear(a, s, w, ws) for a, s in zip(static, scales)))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+sa.linear_status("cuda")
+print("the first calls were captured")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_may_be_captured():
+    """In a process of its own: no operator needs a call before the capture."""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "were captured" in r.stdout, r.stdout + r.stderr

@@ -182,6 +182,7 @@ def test_entry_point_refusals():
     assert call(a_stride=48) == -1 and call(w_stride=48) == -1 and call(out_stride=31) == -1
     assert call(out=0x50001) == -3 and call(a_scale=0x20002) == -3
     assert call(bias=0x60001, bias_dtype=0) == -3 and call(bias=0x60000, bias_dtype=7) == -1
+    assert call(flags=1) == -1 and call(M=2 ** 31 - 1) == -2
     assert call(out=0x10000) == -1 and call(out=0x30000) == -1 and call(out=0x40040) == -1
 
 
@@ -209,3 +210,25 @@ def test_refusals():
     refused("contiguous", lambda: sa.int8_linear(a.t().contiguous().t(), s, w, t))
     refused("no backward", lambda: sa.int8_linear(a, s.clone().requires_grad_(), w, t))
     refused("at least 1", lambda: sa.int8_linear(a[:, :0], s, w[:, :0], t))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(10, 300, 600), (40, 20000, 256), (100, 512, 2000), (300, 300, 500), (4000, 5000, 512)])
+def test_waits_that_run_out(M, N, K):
+    """Products whose tiles never come: every wait gives up, the kernel ends, its output stays as it was, the status
+    says so once, and the next product is right."""
+    import layer_structs as ly
+    from block_sparse_attention_moments_b200 import FLAG_TEST_STALL
+    a, w = rows(M, K, 30), rows(N, K, 31)
+    s, t = scales(M, 32, 0.1), scales(N, 33, 0.01)
+    out = torch.full((M, N), 7.0, device="cuda", dtype=BF16)
+    p = ly.LinearArgs(M, N, K, a.data_ptr(), a.stride(0), s.data_ptr(), w.data_ptr(), w.stride(0), t.data_ptr(), None, 0,
+                      out.data_ptr(), 0, N, FLAG_TEST_STALL)
+    assert sa.lib().sol_attn_quantized_linear(ly.ctypes.byref(p), torch.cuda.current_stream().cuda_stream) == 0
+    with pytest.raises(sa.SolAttnError, match="gave up") as e:
+        sa.linear_status(a.device)
+    assert e.value.code == -5
+    assert (out == 7).all()
+    sa.linear_status(a.device)
+    check(sa.int8_linear(a, s, w, t), a, s, w, t, None)
+    sa.linear_status(a.device)

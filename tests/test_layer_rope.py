@@ -228,6 +228,8 @@ def test_entry_point_refusals():
     assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0x10000)) == -1
     assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0xA0000)) == -1
     assert call(q=ly.RopeTensor(0x10000, 512, 128, 64, 0x90000, 0x50000, 0)) == -1    # a weight without a norm
+    assert call(norm=1, q=ly.RopeTensor(0x10000, 512, 128, 64, 0x90000, 0xA0000, 0)) == -1     # k's output over q's weight
+    assert call(pos_kind=1, positions=0x90000) == -1 and call(pos_kind=1, positions=0x30000, pos_stride_l=-3) == -1
     bad = (c.c_double * 32)(*[math.nan] * 32)
     assert call(freqs=c.addressof(bad)) == -1
     far = (c.c_ubyte * 32)(*[3] * 32)
