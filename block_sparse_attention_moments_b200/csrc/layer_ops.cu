@@ -1,18 +1,14 @@
 // layer_ops.cu — C ABI of the operators around the attention (declared in
-// include/sol_attn.h): argument checks and launches of the norm, rotary and
-// 8-bit product kernels.  They hold no workspace: every call reads its inputs
+// include/sol_attn.h): argument checks in front of the launches.  They hold no workspace: every call reads its inputs
 // and writes its outputs only, so calls on several streams, devices or
 // captured graphs do not meet.
 #include <algorithm>
 #include <climits>
 #include <cmath>
 #include <numeric>
-#include <type_traits>
 
 #include "host.h"
-#include "linear.cuh"
-#include "norm.cuh"
-#include "rope.cuh"
+#include "layer_launch.h"
 
 using namespace solattn;
 
@@ -20,14 +16,6 @@ namespace {
 
 constexpr int kMaxC = 16384;
 constexpr int kMaxLinearK = 131071;   // 128 * 128 * K < 2^31
-constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
-// Tokens up to which channels are the rows of the tile (15360 x 5120: 128 tokens
-// in tiles of 64 23 us, in one tile of 128 rows 37; 5120 x 5120: 200 tokens 19
-// against 16.6 the other way round).
-constexpr int kFewTokens = 128;
-constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
-constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
-constexpr size_t kRopeShared = 220 * 1024;       // shared memory of the rotary kernel
 
 size_t dtype_size(int dtype) { return dtype == SOL_ATTN_FP32 ? 4 : 2; }
 
@@ -115,265 +103,6 @@ int convert(const sol_attn_vectors& v, const char* name, int B, int L, Vectors* 
   out->per = L / v.groups;
   *vec = *vec && vec16(v.data, size, {out->sb, out->sg});
   return SOL_ATTN_OK;
-}
-
-template <typename TX, typename TY, int V, int N, bool RES, int THREADS>
-int launch_norm_as(NormParams p, int sms, cudaStream_t st) {
-  const long long rows = static_cast<long long>(p.B) * p.L;
-  const int per_warp = 32 * N * V;
-  p.warps = (p.C + per_warp - 1) / per_warp;
-  const int teams = std::max(1, 4 / p.warps);
-  const int threads = teams * p.warps * 32;
-  const int blocks = std::max(1, 1024 / threads) * sms;
-  const int grid = static_cast<int>(std::min<long long>((rows + teams - 1) / teams, blocks));
-  norm_kernel<TX, TY, V, N, RES, THREADS><<<grid, threads, 0, st>>>(p);
-  CUDA_TRY(cudaGetLastError());
-  return SOL_ATTN_OK;
-}
-
-template <typename TX, typename TY, int R, bool RES, bool FULL, int WARPS>
-int launch_norm_ring(NormParams p, size_t factors, int dev, int sms, cudaStream_t st) {
-  constexpr int N = kNormRingVectors;
-  const int teams = p.warps > 1 ? std::min(15, kNormRingThreads / 32 / p.warps) : kNormRingThreads / 32;
-  const size_t stage = R == 1 ? 0 : static_cast<size_t>(p.warps) * R * N * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-  const int fit = R == 1 ? teams : static_cast<int>((kNormRingShared - factors) / stage);   // stages of all teams
-  const int used = std::min(teams, fit);
-  p.depth = R == 1 ? 1 : std::min(4, fit / used);
-  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
-  if (!attr_set[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormRingShared)));
-    attr_set[dev] = true;
-  }
-  norm_ring_kernel<TX, TY, R, N, RES, FULL, WARPS><<<sms, used * p.warps * 32, factors + used * p.depth * stage, st>>>(p);
-  CUDA_TRY(cudaGetLastError());
-  return SOL_ATTN_OK;
-}
-
-template <typename TX, typename TY, int R, bool RES, bool FULL>
-int launch_norm_warps(const NormParams& p, size_t factors, int dev, int sms, cudaStream_t st) {
-  return p.warps == 1 ? launch_norm_ring<TX, TY, R, RES, FULL, 1>(p, factors, dev, sms, st)
-                      : launch_norm_ring<TX, TY, R, RES, FULL, 8>(p, factors, dev, sms, st);
-}
-
-template <typename TX, typename TY, bool RES>
-int launch_norm(NormParams p, bool vec, bool wide, int dev, int sms, cudaStream_t st) {
-  if (vec) {
-    // many rows of long groups, whose factors leave room for two teams' rows
-    const long long rows = static_cast<long long>(p.B) * p.L;
-    const int per_warp = 32 * kNormRingVectors * 8;
-    const size_t factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
-    p.warps = (p.C + per_warp - 1) / per_warp;
-    for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
-    if (rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
-        (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift)) {
-      const bool full = p.C % per_warp == 0;
-      if constexpr (sizeof(TX) == 4) {
-        if (factors <= kNormRingShared)
-          return full ? launch_norm_warps<TX, TY, 1, RES, true>(p, factors, dev, sms, st)
-                      : launch_norm_warps<TX, TY, 1, RES, false>(p, factors, dev, sms, st);
-      } else {
-        const size_t stage = static_cast<size_t>(p.warps) * 2 * kNormRingVectors * 32 * 8 * (sizeof(TX) + (RES ? sizeof(TY) : 0));
-        if (full && wide && factors <= kNormRingShared)
-          return launch_norm_warps<TX, TY, 1, RES, true>(p, factors, dev, sms, st);
-        if (factors + 2 * stage <= kNormRingShared)
-          return launch_norm_warps<TX, TY, 2, RES, false>(p, factors, dev, sms, st);
-      }
-    }
-    if (p.C <= 2816) return launch_norm_as<TX, TY, 8, 1, RES, 352>(p, sms, st);
-    if (p.C <= 5120) return launch_norm_as<TX, TY, 8, 1, RES, 640>(p, sms, st);
-    if (p.C <= 8192) return launch_norm_as<TX, TY, 8, 2, RES, 512>(p, sms, st);
-    return launch_norm_as<TX, TY, 8, 4, RES, 512>(p, sms, st);
-  }
-  if (p.C <= 1408) return launch_norm_as<TX, TY, 1, 4, RES, 352>(p, sms, st);
-  if (p.C <= 2560) return launch_norm_as<TX, TY, 1, 4, RES, 640>(p, sms, st);
-  if (p.C <= 8192) return launch_norm_as<TX, TY, 1, 16, RES, 512>(p, sms, st);
-  return launch_norm_as<TX, TY, 1, 32, RES, 512>(p, sms, st);
-}
-
-template <typename TX, typename TY>
-int launch_norm_res(const NormParams& p, bool vec, bool wide, int dev, int sms, cudaStream_t st) {
-  return p.y ? launch_norm<TX, TY, true>(p, vec, wide, dev, sms, st) : launch_norm<TX, TY, false>(p, vec, wide, dev, sms, st);
-}
-
-template <typename T, bool HALF, int WARPS>
-int launch_rope_as(RopeParams p, int dev, int sms, cudaStream_t st) {
-  const int items = p.H * p.d / (HALF ? 16 : 8);
-  const int group = p.d / (HALF ? 16 : 8);
-  p.by_lanes = 32 % group == 0;
-  // per team and parity: cosines and sines, and the items' sums where lanes cannot add them
-  p.team_floats = p.d + (p.norm == kRopeNormHead && !p.by_lanes ? (2 * items + 3) / 4 * 4 : 0);
-  const size_t tables = 2 * p.team_floats * sizeof(float), part = static_cast<size_t>(p.warps) * kRopeVectors * 32 * 8 * sizeof(T);
-  // the widest fp32 rows leave no room for v, and less than that for the weights of a token norm
-  p.staged = p.v.in && tables + 3 * part <= kRopeShared ? 3 : 2;
-  const size_t stage = p.staged * part, per_team = tables + stage;
-  size_t weights = p.norm == kRopeNormNone ? 0 : (p.norm == kRopeNormToken ? p.H : 1) * p.d * 2 * sizeof(float);
-  p.shared_weights = weights + per_team <= kRopeShared;
-  if (!p.shared_weights) weights = 0;
-  int teams = p.warps > 1 ? std::min(15, kRopeThreads / 32 / p.warps) : kRopeThreads / 32;
-  teams = std::max(1, std::min<int>(teams, static_cast<int>((kRopeShared - weights) / per_team)));
-  p.depth = 1;
-  while (p.depth < 4 && weights + teams * (per_team + p.depth * stage) <= kRopeShared) ++p.depth;
-  const size_t smem = weights + teams * (2 * p.team_floats * sizeof(float) + p.depth * stage);
-  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
-  if (!attr_set[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(rope_kernel<T, HALF, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(kRopeShared)));
-    attr_set[dev] = true;
-  }
-  const long long tokens = static_cast<long long>(p.B) * p.L;
-  const int grid = static_cast<int>(std::min<long long>((tokens + teams - 1) / teams, sms));
-  rope_kernel<T, HALF, WARPS><<<grid, teams * p.warps * 32, smem, st>>>(p);
-  CUDA_TRY(cudaGetLastError());
-  return SOL_ATTN_OK;
-}
-
-template <typename T, bool HALF>
-int launch_rope_warps(RopeParams p, int dev, int sms, cudaStream_t st) {
-  const int per_warp = 32 * kRopeVectors * 8;
-  p.warps = (p.H * p.d + per_warp - 1) / per_warp;
-  if (p.warps == 1) return launch_rope_as<T, HALF, 1>(p, dev, sms, st);
-  if (p.warps <= 8) return launch_rope_as<T, HALF, 8>(p, dev, sms, st);
-  return launch_rope_as<T, HALF, 16>(p, dev, sms, st);
-}
-
-template <typename T>
-int launch_rope(const RopeParams& p, int dev, int sms, cudaStream_t st) {
-  return p.half ? launch_rope_warps<T, true>(p, dev, sms, st) : launch_rope_warps<T, false>(p, dev, sms, st);
-}
-
-// 2-D map of rows of K elements (pitch in bytes) with a {box_k, box_rows} box
-// and 128-byte swizzle; what lies outside reads as zero and is not written.
-int make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long K, long long rows,
-                long long pitch, int box_k, int box_rows) {
-  EncodeTiledFn enc;
-  int rc = get_encoder(&enc);
-  if (rc) return rc;
-  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  cuuint64_t gstride[1] = {static_cast<cuuint64_t>(pitch)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, type, 2, const_cast<void*>(ptr), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SOL_ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return SOL_ATTN_OK;
-}
-
-template <typename T>
-constexpr CUtensorMapDataType map_type() {
-  return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-         : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-}
-
-struct LinearOperands {
-  const int8_t* a;
-  long long a_pitch;
-  const int8_t* w;
-  long long w_pitch;
-};
-
-template <int CG, int BN, typename T>
-int launch_linear(const LinearParams& p0, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
-  using C = LinearConfig<CG, BN>;
-  LinearParams p = p0;
-  p.tiles_m = (p.M + 128 * CG - 1) / (128 * CG);
-  p.tiles_n = (p.N + BN - 1) / BN;
-  p.band = 8;
-  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  if (tiles > INT_MAX / 2) return fail(SOL_ATTN_ERR_UNSUPPORTED, "%lld output tiles", tiles);
-  CUtensorMap ma, mw, mo{};
-  int rc;
-  if ((rc = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.a, p.K, p.M, o.a_pitch, 128, 128))) return rc;
-  if ((rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.w, p.K, p.N, o.w_pitch, 128, BN / CG))) return rc;
-  p.direct = reinterpret_cast<uintptr_t>(p.out) % 16 != 0 || p.out_pitch * sizeof(T) % 16 != 0;
-  if (!p.direct &&
-      (rc = make_map_2d(&mo, map_type<T>(), p.out, p.N, p.M, p.out_pitch * sizeof(T), 128 / sizeof(T), 32)))
-    return rc;
-  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
-  if (!attr_set[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(linear_kernel<CG, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(C::kSmem)));
-    attr_set[dev] = true;
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(CG * static_cast<unsigned>(std::min<long long>(tiles, sms / CG)));
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_kernel<CG, BN, T>, ma, mw, mo, p));
-  return SOL_ATTN_OK;
-}
-
-template <int MT, typename T>
-int launch_linear_vec(const LinearParams& p, const LinearOperands& o, int sms, cudaStream_t st) {
-  LinearVecParams v{p, o.a, o.a_pitch, o.w, o.w_pitch, 1};
-  const int groups = (p.N + kVecRows - 1) / kVecRows;
-  if (groups < kVecWarps * 8 * sms) v.split = kVecWarps;
-  const int per_block = kVecWarps / v.split;
-  linear_vec_kernel<MT, T><<<(groups + per_block - 1) / per_block, kVecWarps * 32, 0, st>>>(v);
-  CUDA_TRY(cudaGetLastError());
-  return SOL_ATTN_OK;
-}
-
-template <int BT, typename T>
-int launch_linear_few(LinearParams p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
-  using C = FewConfig<BT>;
-  p.tiles_m = (p.M + BT - 1) / BT;
-  CUtensorMap ma, mw;
-  int rc;
-  if ((rc = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.a, p.K, p.M, o.a_pitch, 128, BT))) return rc;
-  if ((rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.w, p.K, p.N, o.w_pitch, 128, 128))) return rc;
-  static bool attr_set[kMaxDevices] = {false};   // the attribute is set per device
-  if (!attr_set[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(linear_few_kernel<BT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(C::kSmem)));
-    attr_set[dev] = true;
-  }
-  const int tiles = (p.N + 127) / 128 * p.tiles_m, kblocks = (p.K + 127) / 128;
-  int log_split = 0;
-  while (log_split < 3 && (tiles << log_split) < sms && (2 << log_split) <= kblocks) ++log_split;
-  const int split = 1 << log_split;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tiles * split);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_few_kernel<BT, T>, ma, mw, p, log_split));
-  return SOL_ATTN_OK;
-}
-
-template <typename T>
-int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
-  if (p.M == 1) return launch_linear_vec<1, T>(p, o, sms, st);
-  if (p.M == 2) return launch_linear_vec<2, T>(p, o, sms, st);
-  if (p.M <= 4) return launch_linear_vec<4, T>(p, o, sms, st);
-  if (p.M <= 16) return launch_linear_few<16, T>(p, o, dev, sms, st);
-  if (p.M <= 32) return launch_linear_few<32, T>(p, o, dev, sms, st);
-  if (p.M <= kFewTokens) return launch_linear_few<64, T>(p, o, dev, sms, st);
-  // The variant whose slowest SM is done first: waves of tiles, each the time
-  // of its K and of its output.  A block of 128 of K takes both variants the
-  // same 0.35 us, in which an SM is brought its 32 KB; the pair's tile is twice
-  // as wide.  5120 channels of 5120 (us, pair / single): 200 tokens 17.9 / 16.9,
-  // 512 18.6 / 28.6, 1024 32 / 41; 1034 x 1543 x 1000 14.6 / 10.0.
-  const auto cost = [&](int cg, int bn) {
-    const long long tiles = ((p.M + 128LL * cg - 1) / (128 * cg)) * ((p.N + bn - 1LL) / bn);
-    const long long waves = (tiles + sms / cg - 1) / (sms / cg);
-    return waves * ((p.K + 127) / 128 + bn / 64);
-  };
-  if (cost(2, 256) <= cost(1, 128)) return launch_linear<2, 256, T>(p, o, dev, sms, st);
-  return launch_linear<1, 128, T>(p, o, dev, sms, st);
 }
 
 }  // namespace
@@ -488,11 +217,12 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->x.dtype == SOL_ATTN_BF16) return launch_norm_res<__nv_bfloat16, __nv_bfloat16>(p, vec, wide, dev, sms, st);
-  if (a->x.dtype == SOL_ATTN_FP16) return launch_norm_res<__half, __half>(p, vec, wide, dev, sms, st);
-  if (ydt == SOL_ATTN_BF16) return launch_norm_res<float, __nv_bfloat16>(p, vec, wide, dev, sms, st);
-  if (ydt == SOL_ATTN_FP16) return launch_norm_res<float, __half>(p, vec, wide, dev, sms, st);
-  return launch_norm_res<float, float>(p, vec, wide, dev, sms, st);
+  LaunchNorm* const launch = a->x.dtype == SOL_ATTN_BF16   ? launch_norm_bf16
+                             : a->x.dtype == SOL_ATTN_FP16 ? launch_norm_fp16
+                             : ydt == SOL_ATTN_BF16        ? launch_norm_fp32_bf16
+                             : ydt == SOL_ATTN_FP16        ? launch_norm_fp32_fp16
+                                                           : launch_norm_fp32;
+  return launch(p, vec, wide, dev, sms, st);
 }
 
 int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
@@ -597,9 +327,7 @@ int sol_attn_rope(const sol_attn_rope_args* a, void* stream) {
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->dtype == SOL_ATTN_BF16) return launch_rope<__nv_bfloat16>(p, dev, sms, st);
-  if (a->dtype == SOL_ATTN_FP16) return launch_rope<__half>(p, dev, sms, st);
-  return launch_rope<float>(p, dev, sms, st);
+  return launch_rope(p, a->dtype, dev, sms, st);
 }
 
 int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
@@ -647,21 +375,15 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* a, void* stream) {
   int dev, sms;
   if ((rc = device(&dev, &sms))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
-  if (a->out_dtype == SOL_ATTN_BF16) return run_linear<__nv_bfloat16>(p, o, dev, sms, st);
-  if (a->out_dtype == SOL_ATTN_FP16) return run_linear<__half>(p, o, dev, sms, st);
-  return run_linear<float>(p, o, dev, sms, st);
+  return launch_linear(p, o, a->out_dtype, dev, sms, st);
 }
 
 int sol_attn_linear_status(void* stream) {
   int dev, sms, rc;
   if ((rc = device(&dev, &sms))) return rc;
-  auto st = static_cast<cudaStream_t>(stream);
-  CUDA_TRY(cudaStreamSynchronize(st));
   unsigned h = 0;
-  CUDA_TRY(cudaMemcpyFromSymbol(&h, g_linear_status, sizeof(h)));
+  if ((rc = read_linear_status(static_cast<cudaStream_t>(stream), &h))) return rc;
   if (!h) return SOL_ATTN_OK;
-  const unsigned zero = 0;
-  CUDA_TRY(cudaMemcpyToSymbol(g_linear_status, &zero, sizeof(zero)));
   if (h & 1u) return fail(SOL_ATTN_ERR_TIMEOUT, "a bounded device wait of a product gave up (status 0x%x)", h);
   return fail(SOL_ATTN_ERR_DEVICE, "a product's shared memory is not aligned to its tiles (status 0x%x)", h);
 }
