@@ -121,24 +121,14 @@ __device__ __forceinline__ void fold_post(const NormParams& p, int b, int l, int
 
 // Factors in shared memory: a plane of the first four channels of each vector
 // and one of the last four, so that a warp's 16-byte accesses have no conflicts.
-template <int V>
-__device__ __forceinline__ void put_factor(float* plane, int nvec, int vec, const float (&f)[V]) {
-  if constexpr (V == 8) {
-    reinterpret_cast<float4*>(plane)[vec] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(plane)[nvec + vec] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    plane[vec] = f[0];
-  }
+__device__ __forceinline__ void put_factor(float* plane, int nvec, int vec, const float (&f)[8]) {
+  reinterpret_cast<float4*>(plane)[vec] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(plane)[nvec + vec] = make_float4(f[4], f[5], f[6], f[7]);
 }
-template <int V>
-__device__ __forceinline__ void get_factor(const float* plane, int nvec, int vec, float (&f)[V]) {
-  if constexpr (V == 8) {
-    const float4 a = reinterpret_cast<const float4*>(plane)[vec], b = reinterpret_cast<const float4*>(plane)[nvec + vec];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    f[0] = plane[vec];
-  }
+__device__ __forceinline__ void get_factor(const float* plane, int nvec, int vec, float (&f)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(plane)[vec], b = reinterpret_cast<const float4*>(plane)[nvec + vec];
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
 // Normalises R rows that the team holds in registers (no weight or bias).
@@ -518,12 +508,12 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
     for (int vec = threadIdx.x; vec < nvec; vec += blockDim.x) {
       float a[1][V], c[1][V];
       fold_pre<V, 1>(p, b, l0, vec * V, 0, a, c);
-      put_factor<V>(factors, nvec, place(vec), a[0]);
-      put_factor<V>(factors + p.C, nvec, place(vec), c[0]);
+      put_factor(factors, nvec, place(vec), a[0]);
+      put_factor(factors + p.C, nvec, place(vec), c[0]);
       if constexpr (RES) {
         fold_post<V, 1>(p, b, l0, vec * V, 0, a, c);
-        put_factor<V>(factors + 2 * p.C, nvec, place(vec), a[0]);
-        if (p.post_bias.p) put_factor<V>(factors + 3 * p.C, nvec, place(vec), c[0]);
+        put_factor(factors + 2 * p.C, nvec, place(vec), a[0]);
+        if (p.post_bias.p) put_factor(factors + 3 * p.C, nvec, place(vec), c[0]);
       }
     }
     __syncthreads();
@@ -567,8 +557,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
         for (int i = 0; i < N; ++i) {
           if (!on[i]) continue;
           float a[V], c[V];
-          get_factor<V>(factors + 2 * p.C, nvec, factor(i), a);
-          if (p.post_bias.p) get_factor<V>(factors + 3 * p.C, nvec, factor(i), c);
+          get_factor(factors + 2 * p.C, nvec, factor(i), a);
+          if (p.post_bias.p) get_factor(factors + 3 * p.C, nvec, factor(i), c);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             float x[V];
@@ -590,8 +580,8 @@ __global__ void __launch_bounds__(kNormRingThreads, 1) norm_ring_kernel(const __
       }
       emit_rows<TX, TY, R, V, N, RES, WIDE>(p, team, this_row, b, l0 + static_cast<int>(this_row - s0), first, keep, on, v,
                                       [&](int i, float(&a)[V], float(&c)[V]) {
-                                        get_factor<V>(factors, nvec, factor(i), a);
-                                        get_factor<V>(factors + p.C, nvec, factor(i), c);
+                                        get_factor(factors, nvec, factor(i), a);
+                                        get_factor(factors + p.C, nvec, factor(i), c);
                                       });
       if (again) break;
     }
