@@ -9,7 +9,12 @@ namespace solattn {
 namespace {
 
 constexpr size_t kNormRingShared = 220 * 1024;   // shared memory of the ring kernel: factors and rows
-constexpr int kNormRingLeast = 32;               // rows of a block, and of a group, from which it is taken
+// Rows of a block, and tokens of a group, from which the ring kernel is taken
+// (us of norm_kernel and of it: 450 rows of 5120 bf16 7.9 and 6.7, of 1544 4.6
+// and 5.5; 700 of 5120 9.1 and 7.1, of 1024 6.1 and 3.6; 4500 of 5120 37.7 and
+// 21.5; 8000 rows in groups of 4 89 and 89, of 8 77 and 61).
+constexpr int kNormRingRows = 4;
+constexpr int kNormRingGroup = 8;
 constexpr int kNormRingVectors = 4;              // vectors of 8 that a thread holds of a row
 
 template <typename TX, typename TY, int V, int N, bool RES, int THREADS>
@@ -60,7 +65,7 @@ int launch_norm(NormParams p, bool vec, bool wide, int dev, int sms, cudaStream_
     const size_t factors = static_cast<size_t>(RES ? 3 + (p.post_bias.p != nullptr) : 2) * p.C * sizeof(float);
     p.warps = (p.C + per_warp - 1) / per_warp;
     for (p.inner_shift = 0; (1 << p.inner_shift) < p.x_inner;) ++p.inner_shift;
-    if (rows >= kNormRingLeast * static_cast<long long>(sms) && p.group >= kNormRingLeast && p.warps <= 8 &&
+    if (rows >= kNormRingRows * static_cast<long long>(sms) && p.group >= kNormRingGroup && p.warps <= 8 &&
         (p.x_inner == p.C || p.x_inner == 1 << p.inner_shift)) {
       const bool full = p.C % per_warp == 0;
       if constexpr (sizeof(TX) == 4) {

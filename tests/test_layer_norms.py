@@ -379,10 +379,10 @@ def test_refusals():
 
 
 # ------------------------------------------------------------------ many rows
-# From 32 rows of a block on (4736 and more on 148 SMs) another kernel takes the
-# rows, with folded factors in shared memory, two rows at a time and groups whose
-# ends may lie between the two.
-MANY = [(3, 1, 1601, 64), (1, 13, 391, 264), (2, 3, 801, 1024), (5, 1, 1001, 1544), (1, 1, 4737, 2048), (2, 7, 343, 2056),
+# From four rows of a block on (592 on 148 SMs), in groups of eight and more,
+# another kernel takes the rows, with folded factors in shared memory, some two
+# at a time and groups whose ends may lie between the two.
+MANY = [(1, 100, 9, 512), (3, 41, 8, 1544), (1, 37, 17, 5120), (2, 300, 1, 264), (1, 1, 593, 99), (3, 1, 1601, 64), (1, 13, 391, 264), (2, 3, 801, 1024), (5, 1, 1001, 1544), (1, 1, 4737, 2048), (2, 7, 343, 2056),
         (1, 1, 4800, 5120), (3, 50, 33, 1000), (1, 5, 961, 8192)]
 
 
