@@ -96,6 +96,8 @@ int convert(const sol_attn_vectors& v, const char* name, int B, int L, Vectors* 
   const size_t size = dtype_size(v.dtype);
   if (reinterpret_cast<uintptr_t>(v.data) % size)
     return fail(SOL_ATTN_ERR_ALIGN, "%s is not aligned to its elements", name);
+  if ((B > 1 && v.stride_b < 0) || (v.groups > 1 && v.stride_g < 0))
+    return fail(SOL_ATTN_ERR_ARG, "%s has a negative stride", name);
   out->p = v.data;
   out->dtype = v.dtype;
   out->sb = B > 1 ? v.stride_b : 0;

@@ -335,6 +335,7 @@ def test_entry_point_refusals():
     assert call(scale=ly.Vectors(0x50000, 0, 0, 64, 64)) == -1
     assert call(scale=ly.Vectors(0x50000, 9, 1, 64, 64)) == -1
     assert call(scale=ly.Vectors(0x50002, 2, 1, 64, 64)) == -3
+    assert call(scale=ly.Vectors(0x50000, 0, 2, 64, -64)) == -1 and call(gate=ly.Vectors(0x50000, 0, 1, -64, 0)) == -1
     assert call(scale=ly.Vectors(0x90010, 0, 1, 64, 64)) == -1    # h overlaps scale
     assert call(q=0xB0000, q_stride=64) == -1                     # no scales
     assert call(q=0xB0000, q_stride=32, q_scale=0xC0000) == -1
