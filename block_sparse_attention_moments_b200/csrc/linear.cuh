@@ -56,8 +56,8 @@ struct LinearConfig {
   static constexpr int kStageB = BN / CG * 128;
   static constexpr int kStage = kLinStageA + kStageB;
   static constexpr int kOut = 8 * 4096;                  // per output warp 32 rows x 128 bytes
-  static constexpr int kStages = (224 * 1024 - kOut) / kStage > 8 ? 8 : (224 * 1024 - kOut) / kStage;
-  static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kStages = (224 * 1024 - kOut) / kStage;
+  static constexpr int kTmem = 2 * BN;                   // columns of two accumulators
   static constexpr int kParams = BN * 8;                 // the tile's scales and biases, fp32
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kOut + kParams + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
@@ -296,12 +296,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) continue;
       tc_fence_after();
       const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
-      // the last chunk of this warp (of narrow tiles the second warp has none)
-      const int last = BN - kCols >= half * kCols ? (BN / kCols - 1 - half) / 2 * 2 * kCols + half * kCols : -1;
-      if (last < 0 && lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[buf]), 0));
-        else mbar_arrive(&acc_empty[buf]);
-      }
+      static_assert(BN % (2 * kCols) == 0, "both warps of a quarter have as many chunks");
+      const int last = BN - (2 - half) * kCols;
       for (int c0 = half * kCols; c0 < BN; c0 += 2 * kCols) {
         const int col0 = tn * BN + c0;
         uint32_t r[kCols];
