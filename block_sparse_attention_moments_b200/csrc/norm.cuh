@@ -9,7 +9,7 @@
 //   rms    v / sqrt(mean(v^2) + eps) * weight + bias
 //   none   v
 // and h is written as it is, or in 8 bits with a scale for the row:
-//   s = max|h| / 127,  q = round(h / s)
+//   s = max|h| / 127,  q = 127 h / max|h| to the nearest whole number, ties to even
 //
 // Everything between the loads and the stores is fp32 in registers: the row is
 // read once, the variance is the mean square of the centred values (no
@@ -21,7 +21,8 @@
 // Bound by memory where there are many rows.  75600 rows of 5120, share of the
 // copy rate (6.56 TB/s): bf16 norm 266 us (89%), fp32 residual and bf16 output
 // with the next norm 738 us (96%), the same all in bf16 490 us (96%), fp32 to 8
-// bits 310 us (95%), the attention's head-major output to 8 bits 220 us (80%).
+// bits 335 us (88%; a rounding that misses ties took 316), the attention's
+// head-major output to 8 bits 216 us (82%).
 // 10166 rows of 1544 with a group of 391 each take 17.6 us (54%): a launch, the
 // folding of two groups and five turns of each team.  Rows of odd width go
 // element by element: 2062 of 1285 15.7 us (21%).
@@ -243,19 +244,22 @@ __device__ __forceinline__ void emit_rows(const NormParams& p, Team& team, unsig
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (!keep[r]) continue;
-      // q = h * (127 / amax).  A row of zeros has the scale 0 and zeros; one
-      // with an infinity or a NaN a scale that is not finite, and zeros too.
-      // Below 2^-120 the row is scaled up first, as 127 / amax would overflow.
-      float up = 0.f;
-      if (amax[r] >= 0x1p-120f && amax[r] <= 3.402823466e38f) {
-        up = 127.f / amax[r];
+      // A row of zeros has the scale 0 and zeros; one with an infinity or a NaN
+      // a scale that is not finite, and zeros too.  A row whose largest value is
+      // below 2^-100 or above 2^100 is multiplied by a power of two first, so that
+      // 127 / amax and its second term stay in range; what that rounds is far
+      // below a half of a step.
+      Up8 up{0.f, 0.f};
+      if (amax[r] >= 0x1p-100f && amax[r] <= 0x1p100f) {
+        up = up_s8(amax[r]);
       } else {
-        const bool tiny = amax[r] > 0.f && amax[r] < 0x1p-120f;
-        if (tiny) up = 127.f / (amax[r] * 0x1p100f);
+        const bool live = amax[r] > 0.f && amax[r] <= 3.402823466e38f;
+        const float by = !live ? 0.f : amax[r] < 1.f ? 0x1p100f : 0x1p-100f;
+        if (live) up = up_s8(amax[r] * by);
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[r][i][j] = tiny ? v[r][i][j] * 0x1p100f : 0.f;
+          for (int j = 0; j < V; ++j) v[r][i][j] = live ? v[r][i][j] * by : 0.f;
       }
       int8_t* qp = p.q + (row + r) * p.q_sl + first * V;
       if constexpr (WIDE) {
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 352 ? 2 : 1) norm_kernel(c
 // for 16-bit rows that 32-byte vectors do not fill: 16 bytes a vector, and the
 // rows come through a ring of p.depth stages of R rows in shared memory by
 // asynchronous copies, each warp's part by that warp.  75600 x 5120:
-//   fp32 to 8 bits           R = 1 305 us, R = 2 through the ring 454
+//   fp32 to 8 bits           R = 1 335 us; before ties were held 316, ring 454
 //   fp32 with bf16 output    R = 1 737 us, ring 830
 //   bf16                     R = 1 266 us with 32-byte vectors, 362 with 16, ring 287
 // FULL: the teams' threads have exactly the row's vectors.  R rows that a

@@ -197,7 +197,7 @@ __device__ __forceinline__ void mul_v(float (&d)[V], const float (&a)[V]) {
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[j] *= a[j];
+    for (int j = 0; j < V; ++j) d[j] = __fmul_rn(d[j], a[j]);
   }
 }
 template <int V>
@@ -249,24 +249,55 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   return r;
 }
 
-// Values times `up`, to the nearest whole numbers (ties to even), as s8, the
-// first in the lowest byte.  |v * up| <= 127: adding 1.5 * 2^23 leaves the
-// whole number in the low bits of the sum, rounded once.
-__device__ __forceinline__ uint2 pack_s8(const float (&v)[8], float up) {
-  const float2 u = make_float2(up, up), magic = make_float2(12582912.f, 12582912.f);
-  uint32_t k[8];
+// The factor 127 / amax of a row's 8-bit values in two terms, hi rounded and lo
+// what that left out (the residual of a quotient is exact), by 2^-20 too small;
+// amax between 2^-100 and 2^100.
+struct Up8 {
+  float hi, lo;
+};
+__device__ __forceinline__ Up8 up_s8(float amax) {
+  const float hi = 127.f / amax;
+  return Up8{hi, fmaf(-hi, amax, 127.f) * (hi * static_cast<float>((1.0 - 0x1p-20) / 127.0))};
+}
+// v * up to the nearest whole numbers, ties to even, as the low bytes of k: adding
+// 1.5 * 2^23 leaves the whole number there.  hi alone would not do: where
+// 127 v / amax is a half, which is common in rows of 16-bit values (0.2% of normal
+// bf16 ones), v * hi lies beside it, on the same side for a whole row.  So
+//   y = fl(v * hi),  z = fl(y + v * lo).
+// Beside a half h, v * hi = h + E with |E| at most a unit of h, and y = h + R, R
+// being E to the nearest unit (h has few bits, so a tie there falls to h).
+// y + v * lo = h + R - E lies within half a unit of h, and z = h: lo, a little too
+// small, does not carry it beyond.  Values of 11 bits or fewer, bf16 and fp16, thus
+// give the exact result (tried out for every ratio of two of them): no other
+// quotient of theirs is nearer to h = c / 2 than 2^-18 of it, as 254 v - c amax is
+// two units of v's last place at least.  Of other fp32 values one whose quotient is
+// within a unit of a half, 2^-23 of it, may be taken for that half.
+template <int V>
+__device__ __forceinline__ void whole_s8(const float (&v)[V], const Up8& up, uint32_t (&k)[V]) {
+  float lo[V], z[V];
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), u, magic);
-    k[j] = __float_as_uint(r.x), k[j + 1] = __float_as_uint(r.y);
-  }
+  for (int j = 0; j < V; ++j) lo[j] = up.lo, z[j] = v[j];
+  mul_s<V>(z, up.hi);
+  fma_v<V>(z, v, lo, z);
+  add_s<V>(z, 12582912.f);
+#pragma unroll
+  for (int j = 0; j < V; ++j) k[j] = __float_as_uint(z[j]);
+}
+__device__ __forceinline__ uint2 pack_s8(const float (&v)[8], const Up8& up) {
+  uint32_t k[8];
+  whole_s8<8>(v, up, k);
   return make_uint2(__byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(k[4], k[5], 0x0040), __byte_perm(k[6], k[7], 0x0040), 0x5410));
 }
 template <int V>
-__device__ __forceinline__ void store_s8(int8_t* p, const float (&v)[V], float up) {
-  if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = pack_s8(v, up);
-  else *p = static_cast<int8_t>(__float_as_uint(fmaf(v[0], up, 12582912.f)));
+__device__ __forceinline__ void store_s8(int8_t* p, const float (&v)[V], const Up8& up) {
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint2*>(p) = pack_s8(v, up);
+  } else {
+    uint32_t k[1];
+    whole_s8<1>(v, up, k);
+    *p = static_cast<int8_t>(k[0]);
+  }
 }
 
 // N vectors of V consecutive parameters, `step` elements apart, whose type is

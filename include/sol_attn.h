@@ -268,7 +268,9 @@ typedef struct sol_attn_norm_args {
  * with norm(v) = (v - mean) / sqrt(var + eps) * weight + bias (layer),
  * v / sqrt(mean(v^2) + eps) * weight + bias (rms) or v * weight + bias (none).
  * Outputs, each where wanted: x', h, and h in 8 bits: q_scale = max|h| / 127 of
- * the row and q = h * (127 / max|h|) to the nearest whole number, ties to even.  A row
+ * the row and q = 127 h / max|h| to the nearest whole number, ties to even (exactly
+ * for h that 16 bits hold; another h whose quotient is within 2^-23 of a half,
+ * relative to it, may be taken for the half).  A row
  * of zeros has the scale 0; a row that holds an infinity or a NaN has a scale
  * that is not finite and zeros for q. */
 int sol_attn_norm_modulate(const sol_attn_norm_args* args, void* stream);

@@ -496,3 +496,67 @@ def test_many_rows_at_any_alignment(C, dtype):
         assert (out[..., :off] == 3).all() and (out[..., off + C:] == 3).all()
         q, s = sa.quantize_rows(a)
         check_quantised(q, s, x.double(), torch.zeros_like(x, dtype=torch.float64))
+
+
+# ------------------------------------------------------------------ 8-bit values, exactly
+def whole(v):
+    """127 v / max|row| to the nearest whole number, ties to the even one, exactly, and where another neighbour will do.
+    Products of values of 24 bits or fewer by whole numbers below 2^8 are exact in 64 bits, and so is their difference
+    wherever its sign decides.  The quotient is formed with two roundings of half a unit each: what is within a unit of
+    a half c / 2, and not a half, may take either neighbour; a unit is 2^-23 of it at most, so |254 v - c max| <=
+    2^-23 c max there (and 1e-3 of that for terms of 2^-44).  Values of 16 bits are never that near: the difference is
+    zero or two units of v's last place (2^-11 of it or more, v = c max / 254) at least, 2^-18 c max."""
+    v = v.double()
+    a, amax = v.abs(), v.abs().amax(-1, keepdim=True)
+    k = torch.where(amax > 0, torch.floor(127 * a / amax.clamp_min(1e-300)), 0.0)
+    beyond = 254 * a - (2 * k + 1) * amax
+    either = (beyond != 0) & (beyond.abs() <= 1.001 * 2.0 ** -23 * (2 * k + 1) * amax)
+    k = k + ((beyond > 0) | ((beyond == 0) & (k % 2 == 1) & (amax > 0)))
+    return (k * v.sign()).to(torch.int8), either
+
+
+def check_whole(q, want, either, dtype):
+    assert dtype == FP32 or not either.any()
+    assert torch.equal(q[~either], want[~either]), f"{int(((q != want) & ~either).sum())} of {q.numel()} values"
+    assert ((q.int() - want.int()).abs() <= 1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("L,C", [(3, 64), (5, 1285), (40, 5120), (3, 16384), (2000, 1024), (2000, 1000), (1500, 5120), (700, 99)])
+def test_whole_numbers_with_ties(L, C, dtype):
+    """Rows of 16-bit values hold exact halves of the 8-bit step; fp32 rows hold them too, and values a unit beside
+    them.  Rows of very small and very large values hold them at their own scale."""
+    x = randn(2, L, C, dtype=BF16 if dtype == FP32 else dtype)
+    x[0, 0], x[1, L - 1] = x[0, 0] * 2.0 ** (-8 if dtype == FP16 else -115), x[1, L - 1] * 2.0 ** (8 if dtype == FP16 else 115)
+    x = x.to(dtype)
+    if dtype == FP32:
+        row = x[1, 0]
+        row[1:] = row[0].abs() * (2 * (torch.arange(1, C, device="cuda") % 127) + 1) / 254 * row[1:].sign()
+        row[1:] = torch.nextafter(row[1:], torch.where(torch.arange(1, C, device="cuda") % 3 == 0, row[1:], 1e30 * row[1:].sign()))
+    want, either = whole(x)
+    if dtype == BF16 and L >= 700 and C >= 1000:     # there are ties, and some of them have to go down
+        a, amax = x.double().abs(), x.double().abs().amax(-1, keepdim=True)
+        half = (254 * a == (2 * torch.floor(127 * a / amax) + 1) * amax)
+        assert (half & (want.abs() < 127 * a / amax)).any() and (half & (want.abs() > 127 * a / amax)).any()
+    q, _ = sa.quantize_rows(x)
+    check_whole(q, want, either, dtype)
+    if C % 8 == 0:
+        q2, _ = sa.quantize_rows(x.unflatten(2, (8, C // 8)).transpose(1, 2).contiguous().transpose(1, 2))   # by heads
+        assert torch.equal(q2, q)
+    _, q2, _ = sa.gate_residual_norm(torch.zeros_like(x), x, norm="none", quantize=True)
+    assert torch.equal(q2, q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,bits", [(BF16, 8), (FP16, 11)])
+def test_every_ratio_of_16_bit_values(dtype, bits):
+    """A row for each leading part of the largest value, and in it every smaller value that is not rounded to zero."""
+    m = torch.arange(2 ** (bits - 1), 2 ** bits, device="cuda", dtype=torch.float64)
+    smaller = torch.cat([m * 2.0 ** -i for i in range(9)])
+    x = torch.where(smaller <= m[:, None], smaller, 0.0)
+    x = torch.cat([m[:, None], x * torch.where(torch.arange(len(smaller), device="cuda") % 3 == 0, -1, 1)], 1)
+    assert torch.equal(x.to(dtype).double(), x)
+    x = x.to(dtype)
+    want, either = whole(x)
+    check_whole(sa.quantize_rows(x)[0], want, either, dtype)
