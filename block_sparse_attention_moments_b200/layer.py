@@ -110,11 +110,14 @@ def _padded_rows(x, shape):
 
 
 def _placed(fn):
-    """Runs fn with its first tensor's device current and, where a stream is given, with that stream current,
-    so that outputs belong to it; the inputs are marked as used by it."""
+    """Runs fn with the device of its first parameter, a tensor, current and, where a stream is given, with that stream
+    current, so that outputs belong to it; the inputs are marked as used by it.  The tensor is found by its name among
+    keywords; fn refuses a call without one."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        x = args[0] if args else next(iter(kw.values()), None)
+        x = args[0] if args else kw.get(name)
         if isinstance(x, torch.Tensor) and x.is_cuda:
             if stream is not None:
                 return on_stream(x, stream, args, kw)

@@ -188,3 +188,99 @@ def test_first_calls_may_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "were captured" in r.stdout, r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------ streams and devices by keyword
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says that it lies on the second GPU."""
+    is_cuda = True
+    device = torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+    def record_stream(self, stream):
+        stream.recorded.append(self)
+
+
+@pytest.mark.parametrize("order", [("t", "grid"), ("grid", "t"), ("none", "other", "t"), ("stream", "grid", "other", "t")])
+@pytest.mark.parametrize("positional", [False, True])
+def test_the_named_tensor_decides_where_a_call_runs(monkeypatch, order, positional):
+    """Without a GPU: whatever comes first among the keywords, the stream and the device are those of the operator's
+    first parameter, and a call without it runs nowhere."""
+    import contextlib
+
+    from block_sparse_attention_moments_b200 import layer
+    current = []
+
+    @contextlib.contextmanager
+    def entered(x):
+        current.append(x)
+        yield
+        current.pop()
+
+    class Stream:
+        device, recorded = OnDevice.device, []
+
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "device", entered)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(layer, "_current_device", lambda: 0)
+    seen = []
+
+    @layer._placed
+    def operator(t, other=None, *, grid=None, none=None):
+        seen.append(list(current))
+        return t
+
+    t = torch.zeros(4).as_subclass(OnDevice)
+    kw = {"t": t, "other": torch.zeros(2), "grid": (1, 2, 3), "none": None}
+    stream = Stream()
+    kw = {name: stream if name == "stream" else kw[name] for name in order}
+    args = (kw.pop("t"),) if positional else ()
+    kw.pop("stream", None)
+    assert operator(*args, **kw) is t and seen.pop() == [OnDevice.device]
+    assert operator(*args, **kw, stream=stream) is t and seen.pop() == [stream]
+    assert any(r is t for r in stream.recorded)
+    Stream.device = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="stream is on"):
+        operator(*args, **kw, stream=stream)
+    with pytest.raises(TypeError):
+        operator(grid=(1, 2, 3), stream=stream)
+    assert not seen and not current
+
+
+def test_a_stream_is_not_dropped_without_a_tensor():
+    for call in (lambda: sa.norm_modulate(norm="rms", x=torch.zeros(2, 8), stream=object()),
+                 lambda: sa.rope(grid=(1, 1, 1), q=torch.zeros(1, 1, 1, 16), k=None, stream=object()),
+                 lambda: sa.quantize_rows(stream=object(), x=torch.zeros(2, 8))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+@pytest.mark.gpu
+def test_keywords_only_on_a_side_stream(monkeypatch):
+    """Every operator called with keywords only, one that is no tensor first: the library gets the given stream."""
+    from block_sparse_attention_moments_b200 import layer
+    streams, handle = [], layer._raw_stream
+    monkeypatch.setattr(layer, "_raw_stream", lambda device: streams.append(handle(device)) or streams[-1])
+    x = torch.randn(1, 40, 128, device="cuda").to(BF16)
+    q = x.view(1, 40, 2, 64)
+    w, ws = sa.quantize_rows(x[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls = {"norm_modulate": (sa.norm_modulate, dict(norm="rms", scale=None, x=x)),
+             "gate_residual": (sa.gate_residual, dict(residual_scale=0.5, gate=None, y=x, x=x)),
+             "gate_residual_norm": (sa.gate_residual_norm, dict(norm="rms", gate=None, y=x, x=x)),
+             "quantize_rows": (sa.quantize_rows, dict(x=x)),
+             "rope": (sa.rope, dict(grid=(2, 4, 5), norm="head", v=None, k=q, q=q)),
+             "int8_linear": (sa.int8_linear, dict(out_dtype=BF16, w_scale=ws, w=w, a_scale=ws, a=w))}
+    for name, (fn, kw) in calls.items():
+        streams.clear()
+        got = fn(**kw, stream=side)
+        assert streams == [side.cuda_stream], name
+        torch.cuda.synchronize()
+        want = fn(**kw)
+        assert streams[1:] == [torch.cuda.current_stream().cuda_stream], name
+        for a, b in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))):
+            assert torch.equal(a, b), name
