@@ -25,7 +25,7 @@ int launch_rope(const RopeParams& p, int dtype, int dev, int sms, cudaStream_t s
 
 int launch_linear(const LinearParams& p, const LinearOperands& o, int dtype, int dev, int sms, cudaStream_t st);
 
-// Synchronises st, and reads and clears the status word of the products.
+// Reads and clears the status word of the products in one step on st, and synchronises it.
 int read_linear_status(cudaStream_t st, unsigned* status);
 
 }  // namespace solattn

@@ -122,6 +122,8 @@ int launch_linear_few(LinearParams p, const LinearOperands& o, int dev, int sms,
   return SOL_ATTN_OK;
 }
 
+__global__ void take_linear_status(unsigned* taken) { *taken = atomicExch(&g_linear_status, 0u); }
+
 template <typename T>
 int run_linear(const LinearParams& p, const LinearOperands& o, int dev, int sms, cudaStream_t st) {
   if (p.M == 1) return launch_linear_vec<1, T>(p, o, sms, st);
@@ -153,10 +155,19 @@ int launch_linear(const LinearParams& p, const LinearOperands& o, int dtype, int
 }
 
 int read_linear_status(cudaStream_t st, unsigned* status) {
-  CUDA_TRY(cudaStreamSynchronize(st));
-  CUDA_TRY(cudaMemcpyFromSymbol(status, g_linear_status, sizeof(*status)));
-  const unsigned zero = 0;
-  if (*status) CUDA_TRY(cudaMemcpyToSymbol(g_linear_status, &zero, sizeof(zero)));
+  // Taken in one step behind the stream's products, so that what another
+  // stream's product reports meanwhile is left for the next reading, and with
+  // nothing on the default stream, which would wait for unrelated work.
+  cudaStreamCaptureStatus capture;
+  CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  if (capture != cudaStreamCaptureStatusNone) return fail(SOL_ATTN_ERR_STATE, "the stream is being captured: it cannot be synchronised");
+  unsigned* taken = nullptr;
+  CUDA_TRY(cudaMallocAsync(&taken, sizeof(*taken), st));
+  take_linear_status<<<1, 1, 0, st>>>(taken);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(status, taken, sizeof(*taken), cudaMemcpyDeviceToHost, st);
+  const cudaError_t freed = cudaFreeAsync(taken, st), done = cudaStreamSynchronize(st);
+  CUDA_TRY(e != cudaSuccess ? e : freed != cudaSuccess ? freed : done);
   return SOL_ATTN_OK;
 }
 

@@ -398,7 +398,8 @@ def int8_linear(a, a_scale, w, w_scale, bias=None, *, out_dtype=None, out=None):
     a: int8 [M, K] or [B, L, K] with fp32 scales [M] or [B, L], such as (q, s) of quantize_rows or
     norm_modulate(quantize=True); w: int8 [N, K] with fp32 scales [N], such as quantize_rows of a weight matrix.  The
     rows of both start at multiples of 16 bytes (as those calls return them); K is at most 131071.  bias: [N], bf16,
-    fp16 or fp32.  Returns [M, N] or [B, L, N] in out_dtype (bf16, fp16 or fp32; by default bf16)."""
+    fp16 or fp32.  Returns [M, N] or [B, L, N] in out_dtype (bf16, fp16 or fp32; by default bf16).  linear_status tells
+    whether a product's bounded waits held; it is the only sign of one that gave up and left its output unwritten."""
     _input(a, "a", None, _INT8)
     dev = a.get_device()
     _input(w, "w", dev, _INT8)
@@ -440,7 +441,8 @@ def int8_linear(a, a_scale, w, w_scale, bias=None, *, out_dtype=None, out=None):
 
 
 def linear_status(device=None, stream=None):
-    """Synchronises the stream and raises SolAttnError if a product on this device gave up a bounded wait."""
+    """Synchronises the stream (by default the device's current one; no other) and raises SolAttnError if a product gave
+    up a bounded wait: one on that stream, or another of the device that has ended.  A report is given once."""
     with torch.cuda.device(device if stream is None else stream.device):
         _check(lib().sol_attn_linear_status((torch.cuda.current_stream() if stream is None else stream).cuda_stream))
 

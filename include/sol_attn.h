@@ -345,10 +345,12 @@ typedef struct sol_attn_linear_args {
  * The sum is exact in 32-bit integers; the rest is fp32, rounded once. */
 int sol_attn_quantized_linear(const sol_attn_linear_args* args, void* stream);
 
-/* Status of the products enqueued on this device: synchronises stream and
- * returns SOL_ATTN_OK, or SOL_ATTN_ERR_TIMEOUT (and clears the status) if a
- * bounded wait of one of them gave up, whose output is then not valid, or
- * SOL_ATTN_ERR_DEVICE if one refused to run. */
+/* Status of the products on this device: synchronises stream (no other one) and
+ * returns SOL_ATTN_OK, or SOL_ATTN_ERR_TIMEOUT if a bounded wait of a product
+ * gave up, whose output is then not valid, or SOL_ATTN_ERR_DEVICE if one refused
+ * to run.  It tells of every product enqueued on stream before, and of others on
+ * the device that have ended; a report is given once.  SOL_ATTN_ERR_STATE on a
+ * stream that is being captured. */
 int sol_attn_linear_status(void* stream);
 
 #ifdef __cplusplus

@@ -232,3 +232,68 @@ def test_waits_that_run_out(M, N, K):
     sa.linear_status(a.device)
     check(sa.int8_linear(a, s, w, t), a, s, w, t, None)
     sa.linear_status(a.device)
+
+
+# ------------------------------------------------------------------ the status
+def stall(M, N, K, stream):
+    """Enqueues a product whose tiles never come; returns what it reads, to be kept until it has ended."""
+    import layer_structs as ly
+    from block_sparse_attention_moments_b200 import FLAG_TEST_STALL
+    a, w = rows(M, K, 34), rows(N, K, 35)
+    s, t = scales(M, 36, 0.1), scales(N, 37, 0.01)
+    out = torch.zeros((M, N), device="cuda", dtype=BF16)
+    torch.cuda.synchronize()
+    p = ly.LinearArgs(M, N, K, a.data_ptr(), a.stride(0), s.data_ptr(), w.data_ptr(), w.stride(0), t.data_ptr(), None, 0,
+                      out.data_ptr(), 0, N, FLAG_TEST_STALL)
+    assert sa.lib().sol_attn_quantized_linear(ly.ctypes.byref(p), stream.cuda_stream) == 0
+    return a, w, s, t, out
+
+
+@pytest.mark.gpu
+def test_status_waits_for_its_stream_only():
+    """The status of one stream, while the default stream is busy for about a second."""
+    side = torch.cuda.Stream()
+    keep = stall(300, 300, 500, side)
+    torch.cuda._sleep(2_000_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    with pytest.raises(sa.SolAttnError, match="gave up"):
+        sa.linear_status(stream=side)
+    sa.linear_status(stream=side)
+    assert not busy.query()
+    torch.cuda.synchronize()
+    del keep
+
+
+@pytest.mark.gpu
+def test_status_of_products_that_end_while_it_is_read():
+    """Readings on another stream while a product gives up: it is reported by one of them, or by the one behind it."""
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        keep = stall(300, 300, 500, side)
+        reports = 0
+        for stream in [other] * 50 + [side]:
+            try:
+                sa.linear_status(stream=stream)
+            except sa.SolAttnError as e:
+                assert e.code == -5
+                reports += 1
+        assert reports
+        del keep
+    sa.linear_status(stream=side)
+
+
+@pytest.mark.gpu
+def test_status_is_refused_in_a_capture():
+    """And the capture goes on."""
+    a, w = rows(40, 64, 38), rows(32, 64, 39)
+    s, t = scales(40, 40, 1.0), scales(32, 41, 1.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = sa.int8_linear(a, s, w, t)
+        with pytest.raises(sa.SolAttnError, match="captured") as e:
+            sa.linear_status(a.device)
+        assert e.value.code == -6
+    graph.replay()
+    assert torch.equal(y, sa.int8_linear(a, s, w, t))
+    sa.linear_status(a.device)
