@@ -7,8 +7,10 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
+#include <vector>
 
 #include "fused.cuh"
 #include "host.h"
@@ -36,6 +38,8 @@ struct Shape {
 struct Workspace {
   void* base = nullptr;
   size_t bytes = 0;
+  bool captured = false;      // a captured graph refers to base: growing leaves it allocated,
+  std::vector<void*> kept;    // here, until the workspace is released
   // carved views
   float* qbar = nullptr;
   float* kbar = nullptr;
@@ -116,7 +120,16 @@ int ensure_ws(const Shape& s, Workspace** out) {
   }
   const size_t need = layout(s, nullptr, nullptr);
   if (need > w.bytes) {
-    if (w.base) CUDA_TRY(cudaFree(w.base));
+    if (w.captured) {
+      try {
+        w.kept.push_back(w.base);
+      } catch (const std::exception&) {
+        return fail(SOL_ATTN_ERR_CUDA, "no host memory to keep a captured workspace");
+      }
+      w.captured = false;
+    } else if (w.base) {
+      CUDA_TRY(cudaFree(w.base));
+    }
     w.base = nullptr;
     w.bytes = 0;
     CUDA_TRY(cudaMalloc(&w.base, need));
@@ -129,6 +142,16 @@ int ensure_ws(const Shape& s, Workspace** out) {
     w.stage = 0;
   }
   *out = &w;
+  return SOL_ATTN_OK;
+}
+
+// To be called before work on the workspace is enqueued on st.  (The default
+// stream cannot be captured.)
+int note_capture(Workspace& w, cudaStream_t st) {
+  if (!st || w.captured) return SOL_ATTN_OK;
+  cudaStreamCaptureStatus capture;
+  CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  w.captured = capture != cudaStreamCaptureStatusNone;
   return SOL_ATTN_OK;
 }
 
@@ -389,6 +412,7 @@ int sol_attn_forward_ex(const void* q, const void* k, const void* v, void* out, 
   Workspace* w;
   if ((rc = ensure_ws(Shape{B, H, L, d}, &w))) return rc;
   auto st = static_cast<cudaStream_t>(stream);
+  if ((rc = note_capture(*w, st))) return rc;
   if ((rc = run_pool(*w, q, k, v, dbg, st))) return rc;
   if ((rc = run_threshold(*w, beta, flags, dbg, st))) return rc;
   if ((rc = run_fused(*w, q, k, v, out, chunk, flags, dbg, st))) return rc;
@@ -409,7 +433,9 @@ int sol_attn_stage_pool(const void* q, const void* k, const void* v, int B, int 
   std::lock_guard<std::mutex> lk(g_mu);
   Workspace* w;
   if ((rc = ensure_ws(Shape{B, H, L, d}, &w))) return rc;
-  return run_pool(*w, q, k, v, dbg, static_cast<cudaStream_t>(stream));
+  auto st = static_cast<cudaStream_t>(stream);
+  if ((rc = note_capture(*w, st))) return rc;
+  return run_pool(*w, q, k, v, dbg, st);
 }
 
 int sol_attn_stage_threshold(int B, int H, int L, int d, int block, float beta, unsigned flags,
@@ -423,7 +449,9 @@ int sol_attn_stage_threshold(int B, int H, int L, int d, int block, float beta, 
   Workspace& w = g_ws[dev];
   if (!(w.shape == Shape{B, H, L, d}) || w.stage < 1)
     return fail(SOL_ATTN_ERR_STATE, "stage_threshold needs a stage_pool of the same shape first");
-  return run_threshold(w, beta, flags, dbg, static_cast<cudaStream_t>(stream));
+  auto st = static_cast<cudaStream_t>(stream);
+  if ((rc = note_capture(w, st))) return rc;
+  return run_threshold(w, beta, flags, dbg, st);
 }
 
 int sol_attn_stage_fused(const void* q, const void* k, const void* v, void* out, int B, int H, int L, int d, int block,
@@ -441,6 +469,7 @@ int sol_attn_stage_fused(const void* q, const void* k, const void* v, void* out,
   if (!(w.shape == Shape{B, H, L, d}) || w.stage < 2)
     return fail(SOL_ATTN_ERR_STATE, "stage_fused needs stage_pool and stage_threshold of the same shape first");
   auto st = static_cast<cudaStream_t>(stream);
+  if ((rc = note_capture(w, st))) return rc;
   if ((rc = run_fused(w, q, k, v, out, chunk, flags, dbg, st))) return rc;
   if (flags & SOL_ATTN_FLAG_SYNC_CHECK) return read_status(w, st);
   return SOL_ATTN_OK;
@@ -550,6 +579,7 @@ int sol_attn_release(void) {
   if ((rc = current_device(&dev))) return rc;
   Workspace& w = g_ws[dev];
   if (w.base) CUDA_TRY(cudaFree(w.base));
+  for (void* p : w.kept) CUDA_TRY(cudaFree(p));
   if (w.ctl_block) CUDA_TRY(cudaFree(w.ctl_block));
   if (w.host_stage) CUDA_TRY(cudaFree(w.host_stage));
   if (w.topk_map) CUDA_TRY(cudaFree(w.topk_map));

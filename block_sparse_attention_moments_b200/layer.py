@@ -483,7 +483,8 @@ class AttentionLayer:
         """x: [B, L, C], bf16 or fp32; scale, shift, gate, next_scale, next_shift: vectors as norm_modulate takes
         them; beta, chunk, flags: the attention's; grid, positions, start: rope's.  Returns (x', h') with h' in
         bf16; x_out=x updates the stream in place.  Runs on the current stream of x's device; the attention's
-        workspace is the device's, so calls on one device must not overlap."""
+        workspace is the device's, so calls on one device must not overlap, replays of captured ones among them, and
+        the first call of a shape must not be captured.  linear_status tells whether the products' waits held."""
         _input(x, "x", self.w_qkv.get_device(), (torch.bfloat16, torch.float32))
         if x.dim() != 3 or x.shape[2] != self.w_qkv.shape[1]:
             raise ValueError(f"x must be [B, L, {self.w_qkv.shape[1]}] (got {list(x.shape)})")

@@ -32,7 +32,10 @@
  *     per-row counts, a work counter and a status word) that grows on demand
  *     with cudaMalloc; the first call for a larger shape therefore must not be
  *     inside a stream capture.  Calls on one device share the workspace: do
- *     not run two forwards concurrently on different streams of one device.
+ *     not run two forwards concurrently on different streams of one device,
+ *     replays of captured ones among them.  A captured forward keeps the block
+ *     that it was captured with: growing leaves that allocated until
+ *     sol_attn_release, after which the graph must not be replayed.
  *   - Return value: SOL_ATTN_OK (0) or a negative sol_attn_status code.
  *     sol_attn_error_string() describes the last error in words.
  */

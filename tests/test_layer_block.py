@@ -284,3 +284,30 @@ def test_keywords_only_on_a_side_stream(monkeypatch):
         assert streams[1:] == [torch.cuda.current_stream().cuda_stream], name
         for a, b in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))):
             assert torch.equal(a, b), name
+
+
+@pytest.mark.gpu
+def test_a_captured_layer_outlives_a_larger_call():
+    """A captured layer is replayed after a forward that needs a larger workspace, and after smaller ones."""
+    B, L, H, d, grid = 1, 700, 2, 128, (7, 10, 10)
+    x, w, vectors = make(B, L, H, d, BF16, 2)
+    shift, scale, gate, next_shift, next_scale = vectors
+    layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], H, b_qkv=w["b_qkv"], b_out=w["b_out"])
+    kw = dict(beta=0.5, chunk=8, grid=grid, next_scale=next_scale, next_shift=next_shift)
+    torch.cuda.synchronize()
+    sa.release()
+    want = layer(x, scale, shift, gate, **kw)        # the workspace is this shape's
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer(x, scale, shift, gate, **kw)
+    for shape in ((1, 8, 5000, 128), (1, 1, 70, 64), (2, 8, 9000, 128)):
+        q, k, v = (torch.randn(shape, device="cuda").to(BF16) for _ in range(3))
+        first = sa.forward(q, k, v, 0.5, 8)
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert torch.equal(sa.forward(q, k, v, 0.5, 8), first)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    del graph
+    sa.release()
