@@ -29,10 +29,15 @@ inline int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+// A failure is reported once: the runtime's record of it is cleared, or the next
+// launch's check, this library's or its caller's, would take it for its own.
 #define CUDA_TRY(expr)                                                                        \
   do {                                                                                        \
     cudaError_t e_ = (expr);                                                                  \
-    if (e_ != cudaSuccess) return fail(SOL_ATTN_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_)); \
+    if (e_ != cudaSuccess) {                                                                  \
+      cudaGetLastError();                                                                     \
+      return fail(SOL_ATTN_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_));                \
+    }                                                                                         \
   } while (0)
 
 inline int current_device(int* dev) {

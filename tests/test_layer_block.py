@@ -311,3 +311,27 @@ def test_a_captured_layer_outlives_a_larger_call():
     torch.cuda.synchronize()
     del graph
     sa.release()
+
+
+def no_room():
+    """A workspace of terabytes: the allocator refuses it before anything is read or enqueued."""
+    B, H, L, d = 1, 65535, 2 ** 20, 128
+    assert sa.workspace_bytes(B, H, L, d) > 2 ** 40
+    far = [2 ** 40 + i * 2 * B * H * L * d for i in range(3)]
+    with pytest.raises(sa.SolAttnError) as e:
+        sa._check(sa.lib().sol_attn_stage_pool(*far, B, H, L, d, 64, None, torch.cuda.current_stream().cuda_stream))
+    assert e.value.code == -4 and "memory" in str(e.value)
+
+
+@pytest.mark.gpu
+def test_a_failed_call_does_not_fail_the_next():
+    x = torch.randn(3, 64, device="cuda")
+    want = sa.norm_modulate(x)
+    torch.cuda.synchronize()
+    sa.release()
+    no_room()
+    assert torch.equal(sa.norm_modulate(x), want)
+    no_room()
+    x.add_(1)
+    torch.cuda.synchronize()
+    sa.release()
