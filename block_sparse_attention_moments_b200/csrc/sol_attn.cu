@@ -132,6 +132,8 @@ int ensure_ws(const Shape& s, Workspace** out) {
     }
     w.base = nullptr;
     w.bytes = 0;
+    w.shape = Shape{};   // no views into the old block are left, also where there is no room for a new one
+    w.stage = 0;
     CUDA_TRY(cudaMalloc(&w.base, need));
     w.bytes = need;
     CUDA_TRY(cudaMemset(w.base, 0, need));

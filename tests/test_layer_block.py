@@ -335,3 +335,19 @@ def test_a_failed_call_does_not_fail_the_next():
     x.add_(1)
     torch.cuda.synchronize()
     sa.release()
+
+
+@pytest.mark.gpu
+def test_a_shape_that_finds_no_room_leaves_no_views():
+    """The shape before it then gets a block, and views, of its own."""
+    q, k, v = (torch.randn(1, 2, 300, 64, device="cuda").to(BF16) for _ in range(3))
+    torch.cuda.synchronize()
+    sa.release()
+    want = sa.forward(q, k, v, 0.5, 8)
+    no_room()
+    with pytest.raises(sa.SolAttnError) as e:
+        sa.stats(1, 2, 300)
+    assert e.value.code == -6
+    assert torch.equal(sa.forward(q, k, v, 0.5, 8), want)
+    torch.cuda.synchronize()
+    sa.release()
