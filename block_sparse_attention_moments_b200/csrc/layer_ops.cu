@@ -49,21 +49,23 @@ Span span(const void* p, size_t size, long long sb, long long sl, int B, int L, 
   return Span{static_cast<const char*>(p), B > 1 ? sb * s : 0, L > 1 ? sl * s : 0, B, L, width * s};
 }
 
-// Whether two sets of rows share a byte.  Rows of equal pitch whose columns
-// lie side by side do not (two slices of one buffer); any other two whose
-// address ranges meet are taken to.
+// Whether two sets of rows share a byte.  Where all of their strides are
+// multiples of one pitch and the columns lie side by side within it, they do not
+// (two slices of one buffer); any other two whose address ranges meet are taken
+// to.
 bool overlap(const Span& a, const Span& b) {
   if (a.end() <= b.p || b.end() <= a.p) return false;
-  if (a.sl == b.sl && a.sb == b.sb && a.L > 1) {
-    const long long d = ((b.p - a.p) % a.sl + a.sl) % a.sl;
-    if (a.sb % a.sl == 0 && d >= a.width && d + b.width <= a.sl) return false;
-  }
-  return true;
+  long long pitch = 0;
+  for (long long s : {a.sb, a.sl, b.sb, b.sl})
+    if (s && (!pitch || s < pitch)) pitch = s;
+  if (!pitch || a.sb % pitch || a.sl % pitch || b.sb % pitch || b.sl % pitch) return true;
+  const long long d = ((b.p - a.p) % pitch + pitch) % pitch;
+  return d < a.width || d + b.width > pitch;
 }
 
 // Rows that are written: distinct rows may not share elements.
 bool rows_distinct(const Span& s) {
-  if (s.L > 1 && s.sl < s.width) return s.B > 1 && s.sb >= s.width && s.sl >= (s.B - 1) * s.sb + s.width;
+  if (s.L > 1 && s.sl < s.width) return false;
   return s.B <= 1 || s.sb >= (s.L - 1) * s.sl + s.width ||
          (s.sb >= s.width && s.sl >= (s.B - 1) * s.sb + s.width);
 }
@@ -150,7 +152,7 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
   if (p.x_sh < 0) return fail(SOL_ATTN_ERR_ARG, "x has a negative stride");
   bool vec = C % 8 == 0 && p.x_inner % 8 == 0 && vec8(p.x, xs, {p.x_sb, p.x_sl, p.x_sh});
   const Span x = span(p.x, xs, p.x_sb, p.x_sl, B, L, (C / p.x_inner - 1) * p.x_sh + p.x_inner);
-  Span y{}, outs[3];
+  Span y{}, outs[4];
   int nouts = 0;
   if (a->y.data) {
     p.y = a->y.data, p.y_sb = B > 1 ? a->y.stride_b : 0, p.y_sl = L > 1 ? a->y.stride_l : 0;
@@ -185,8 +187,9 @@ int sol_attn_norm_modulate(const sol_attn_norm_args* a, void* stream) {
     p.q = a->q, p.q_sl = a->q_stride, p.q_scale = a->q_scale;
     vec = vec && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.q_sl % 8 == 0;
     outs[nouts++] = span(p.q, 1, p.q_sl * L, p.q_sl, B, L, C);
-    if (overlap(outs[nouts - 1], x) || (p.y && overlap(outs[nouts - 1], y)))
-      return fail(SOL_ATTN_ERR_ARG, "q overlaps an input");
+    outs[nouts++] = span(p.q_scale, sizeof(float), 0, 0, 1, 1, static_cast<long long>(B) * L);
+    for (int i = nouts - 2; i < nouts; ++i)
+      if (overlap(outs[i], x) || (p.y && overlap(outs[i], y))) return fail(SOL_ATTN_ERR_ARG, "q or q_scale overlaps an input");
   }
   for (int i = 0; i < nouts; ++i)
     for (int j = 0; j < i; ++j)

@@ -560,3 +560,42 @@ def test_every_ratio_of_16_bit_values(dtype, bits):
     x = x.to(dtype)
     want, either = whole(x)
     check_whole(sa.quantize_rows(x)[0], want, either, dtype)
+
+
+# ------------------------------------------------------------------ memory that inputs and outputs share
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,L", [(3, 1), (1, 1), (1, 4), (3, 4)])
+@pytest.mark.parametrize("batch_first", [True, False])
+def test_slices_of_one_buffer(B, L, batch_first):
+    """Columns side by side in one buffer, token-major or batch-major, are read and written; columns that meet are not."""
+    C = 40
+    buf = randn(B, L, 2 * C, dtype=BF16) if batch_first else randn(L, B, 2 * C, dtype=BF16).transpose(0, 1)
+    x, out = buf[..., :C], buf[..., C:]
+    kept = x.clone()
+    want = sa.norm_modulate(kept)
+    assert sa.norm_modulate(x, out=out) is out
+    assert torch.equal(out, want) and torch.equal(x, kept)
+    want_x, want_h = sa.gate_residual_norm(kept, kept)
+    both = torch.zeros(B, L, 4 * C, device="cuda", dtype=BF16)
+    sa.gate_residual_norm(both[..., :C].copy_(kept), kept, x_out=both[..., C:2 * C], out=both[..., 3 * C:])
+    assert torch.equal(both[..., C:2 * C], want_x) and torch.equal(both[..., 3 * C:], want_h) and not both[..., 2 * C:3 * C].any()
+    with pytest.raises(sa.SolAttnError, match="overlap"):
+        sa.norm_modulate(x, out=buf[..., C - 1:2 * C - 1])
+    with pytest.raises(sa.SolAttnError, match="overlap"):
+        sa.norm_modulate(out, out=buf[..., 1:C + 1])
+    with pytest.raises(sa.SolAttnError, match="overlap"):
+        sa.gate_residual_norm(kept, kept, x_out=both[..., C:2 * C], out=both[..., 2 * C - 1:3 * C - 1])
+
+
+def test_the_scales_of_rows_overlap_nothing():
+    """Refused before anything is read."""
+    import layer_structs as ly
+
+    def call(q_scale):
+        a = ly.NormArgs(B=2, L=4, C=64, x_inner=64, x=ly.Rows(0x10000, 0, 256, 64), y=ly.Rows(0x30000, 0, 256, 64),
+                        x_out=ly.Rows(0x50000, 0, 256, 64), h=ly.Rows(0x70000, 0, 256, 64), q=0x90000, q_stride=64,
+                        q_scale=q_scale, residual_scale=1.0, norm=1, eps=1e-6, scale=ly.Vectors(0xB0000, 2, 1, 64, 0))
+        return sa.lib().sol_attn_norm_modulate(ly.ctypes.byref(a), None)
+
+    for at in (0x10000, 0x303FC, 0x50010, 0x703F0, 0x90100, 0xB0080):
+        assert call(at) == -1 and "overlap" in sa.lib().sol_attn_error_string(-1).decode()
