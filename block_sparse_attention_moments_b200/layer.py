@@ -493,7 +493,7 @@ class AttentionLayer:
             h, h_scale = norm_modulate(x, scale, shift, norm=self.norm, eps=self.eps, quantize=True)
             qkv = int8_linear(h, h_scale, self.w_qkv, self.w_qkv_scale, self.b_qkv).view(B, L, 3, self.heads, self.d)
             q, k, v = rope(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], grid=grid, positions=positions, start=start, **self.rope)
-            o = forward(q, k, v, beta, chunk, flags=flags)
+            o = forward(q, k, v, beta, chunk, flags=flags) if B and L else q
             o8, o_scale = quantize_rows(o.transpose(1, 2))
             y = int8_linear(o8, o_scale, self.w_out, self.w_out_scale, self.b_out)
             return gate_residual_norm(x, y, gate, next_scale, next_shift, norm=self.norm, eps=self.eps, x_out=x_out)

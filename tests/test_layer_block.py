@@ -351,3 +351,12 @@ def test_a_shape_that_finds_no_room_leaves_no_views():
     assert torch.equal(sa.forward(q, k, v, 0.5, 8), want)
     torch.cuda.synchronize()
     sa.release()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,L", [(1, 0), (0, 5), (0, 0)])
+def test_layer_without_tokens(B, L):
+    x, w, _ = make(1, 1, 2, 64, FP32)
+    layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], 2)
+    xn, h = layer(torch.empty(B, L, 128, device="cuda"), beta=1.0, chunk=4, grid=(1, 1, 1))
+    assert xn.shape == h.shape == (B, L, 128) and xn.dtype == FP32 and h.dtype == BF16
