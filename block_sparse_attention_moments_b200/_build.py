@@ -42,44 +42,81 @@ def _deps(source: str):
     return [os.path.join(CSRC, source), *_COMMON, *(_ATTN if source == "sol_attn.cu" else _LAYER)]
 
 
-def _older(path: str, deps) -> bool:
-    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in deps)
+def _fresh(path: str, deps, key: str) -> bool:
+    """Whether path is at least as new as what it is made of, and was made with these flags (kept beside it)."""
+    if not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in deps):
+        return False
+    try:
+        with open(path + ".flags") as f:
+            return f.read() == key
+    except OSError:
+        return False
 
 
-def is_stale(lib: str = LIB) -> bool:
-    return _older(lib, {f for _, source, _ in UNITS for f in _deps(source)})
+def _units(extra_flags, profile: bool):
+    """(object, source, flags) of each unit."""
+    for name, source, defines in UNITS:
+        mine = profile and source == "sol_attn.cu"
+        yield (os.path.join(OBJ, f"{name}_profile.o" if mine else f"{name}.o"), source,
+               [*NVCC_FLAGS, *extra_flags, *defines, *(["-DSOL_ATTN_PROFILE"] if mine else [])])
 
 
-def _run(cmd, verbose: bool):
+def _unit_key(source: str, flags) -> str:
+    return " ".join([source, *flags])   # no paths: a copy of the tree elsewhere stays fresh
+
+
+def _lib_key(units) -> str:
+    return "\n".join([" ".join([*NVCC_FLAGS, "-shared"]), *(_unit_key(source, flags) for _, source, flags in units)])
+
+
+def is_stale(lib: str = None, extra_flags=()) -> bool:
+    lib = lib or LIB
+    units = list(_units(extra_flags, lib == PROFILE_LIB))
+    return not _fresh(lib, {f for _, source, _ in units for f in _deps(source)}, _lib_key(units))
+
+
+def _make(path: str, key: str, flags, inputs, verbose: bool):
+    """Compiles into a file of its own, which takes path's place once it is whole."""
+    part = f"{path}.{os.getpid()}.part"
+    cmd = [nvcc_path(), *flags, "-o", part, *inputs]
     if verbose:
         print(" ".join(cmd))
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+        if os.path.exists(path + ".flags"):
+            os.remove(path + ".flags")   # until the new ones stand there, path is not fresh
+        os.replace(part, path)
+    finally:
+        if os.path.exists(part):
+            os.remove(part)
+    with open(part, "w") as f:
+        f.write(key)
+    os.replace(part, path + ".flags")
     if verbose and (r.stdout or r.stderr):
         print(r.stdout, r.stderr)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), profile: bool = False) -> str:
     """Build libsol_attn.so (or, with profile=True, libsol_attn_profile.so with the
-    fused kernel's cycle accounting compiled in).  The units are compiled side by
-    side; the two libraries share the objects of the layer operators."""
+    fused kernel's cycle accounting compiled in).  What is older than its sources, or was
+    made with other flags, is compiled, side by side; force compiles all of it, but that
+    the profiling library takes the regular one's objects where they are fresh."""
     lib = PROFILE_LIB if profile else LIB
-    if not force and not is_stale(lib):
+    if not force and not is_stale(lib, extra_flags):
         return lib
     os.makedirs(OBJ, exist_ok=True)
-    objects, jobs = [], []
-    for name, source, defines in UNITS:
-        mine = profile and source == "sol_attn.cu"
-        obj = os.path.join(OBJ, f"{name}_profile.o" if mine else f"{name}.o")
-        objects.append(obj)
-        # the profiling library takes the regular build's objects where they are up to date
-        if (force and not (profile and not mine)) or _older(obj, _deps(source)):
-            jobs.append([nvcc_path(), "-c", *NVCC_FLAGS, *extra_flags, *defines, *(["-DSOL_ATTN_PROFILE"] if mine else []),
-                         "-I", os.path.join(ROOT, "include"), "-o", obj, os.path.join(CSRC, source)])
+    units = list(_units(extra_flags, profile))
+    jobs = []
+    for obj, source, flags in units:
+        shared = profile and "-DSOL_ATTN_PROFILE" not in flags
+        key = _unit_key(source, flags)
+        if (force and not shared) or not _fresh(obj, _deps(source), key):
+            jobs.append((obj, key, ["-c", *flags, "-I", os.path.join(ROOT, "include")], [os.path.join(CSRC, source)]))
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
-        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
-    _run([nvcc_path(), *NVCC_FLAGS, "-shared", "-o", lib, *objects], verbose)
+        list(pool.map(lambda job: _make(*job, verbose), jobs))
+    _make(lib, _lib_key(units), [*NVCC_FLAGS, "-shared"], [obj for obj, _, _ in units], verbose)
     return lib
 
 
