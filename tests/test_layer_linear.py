@@ -297,3 +297,48 @@ def test_status_is_refused_in_a_capture():
     graph.replay()
     assert torch.equal(y, sa.int8_linear(a, s, w, t))
     sa.linear_status(a.device)
+
+
+# ------------------------------------------------------------------ large products
+# Of these sizes the tiles of two SMs are taken (on 148 SMs), in several bands of tokens, with ragged edges.  The weights
+# of the second one are larger than what is kept in L2 beside the rest.
+LARGE = [(4099, 5001, 384), (4500, 6001, 6000), (5003, 4001, 1000)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_and_ragged(M, N, K, dtype):
+    """Odd numbers of channels, so that output rows are at no multiple of 16 bytes, rows at such multiples with an odd
+    end, and an output tensor at an odd place; the same bits in all."""
+    a, w = rows(M, K, 50), rows(N, K, 51)
+    s, t = scales(M, 52, 0.01), scales(N, 53, 0.01 / math.sqrt(K))
+    bias = torch.randn(N, device="cuda").to(dtype)
+    out = sa.int8_linear(a, s, w, t, bias, out_dtype=dtype)
+    check(out, a, s, w, t, bias)
+    even = N // 8 * 8
+    assert torch.equal(sa.int8_linear(a, s, w[:even], t[:even], bias[:even], out_dtype=dtype), out[:, :even])
+    odd = torch.full((M * N + 2,), 5.0, device="cuda", dtype=dtype)
+    assert torch.equal(sa.int8_linear(a, s, w, t, bias, out=odd[1:-1].view(M, N)), out) and odd[0] == 5 and odd[-1] == 5
+    sa.linear_status(a.device)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_rows_of_large_products_do_not_depend_on_their_neighbours(M, N, K):
+    """The same bits through the kernels for one to four tokens, for up to 128, for single SMs and for pairs."""
+    a, w = rows(M, K, 54), rows(N, K, 55)
+    s, t = scales(M, 56, 0.1), scales(N, 57, 0.01)
+    whole = sa.int8_linear(a, s, w, t)
+    for first, n in ((0, 1), (255, 2), (M - 4, 4), (250, 12), (1000, 30), (M - 128, 128), (127, 130), (4095, 4), (M - 300, 300)):
+        assert torch.equal(sa.int8_linear(a[first:first + n], s[first:first + n], w, t), whole[first:first + n]), (first, n)
+    n = 520
+    assert torch.equal(sa.int8_linear(a, s, w[:n], t[:n]), whole[:, :n])
+
+
+@pytest.mark.gpu
+def test_the_longest_sums_of_large_products():
+    M, N, K = 513, 9000, 131071
+    a, w = rows(M, K, 0, full=True), rows(N, K, 0, full=True)
+    one = torch.ones(N, device="cuda")
+    assert (sa.int8_linear(a, one[:M], w, one, out_dtype=FP32) == float(128 * 128 * K)).all()
