@@ -43,10 +43,18 @@ int launch_linear_tiles(const LinearParams& p0, const LinearOperands& o, int dev
   LinearParams p = p0;
   p.tiles_m = (p.M + 128 * CG - 1) / (128 * CG);
   p.tiles_n = (p.N + BN - 1) / BN;
-  // Tiles of M that share each tile of the weights while it lies in L2.
-  // 75600 x 15360 x 5120, us with 2, 4, 8, 16, 32: 4215, 4153, 3920, 3818, 3844;
-  // 75600 x 5120 x 5120: 1216, 1272, 1262, 1290, 1285 (a run apart by 2%).
-  p.band = 16;
+  // Tiles of M that share each tile of the weights while it lies in L2.  Weights
+  // that stay there whole, a quarter of its 126 MB or less, want narrow bands, whose
+  // tokens are read once; larger ones pass through L2 once a band.  us with
+  // 2, 4, 8, 16, 32 (rows x channels x K, MB of weights):
+  //   16  32768 x  2048 x  8192   340   340   342   352   380
+  //   18  32768 x  9216 x  2048   417   418   423   425   422
+  //   25  75600 x  5120 x  5120  1207  1213  1222  1236  1243
+  //   64   8192 x  8192 x  8192   374   356   345   336   366
+  //   67  75600 x  5120 x 13824  3554  3587  3419  3447  3711
+  //   75  75600 x 15360 x  5120  4015  4004  3783  3672  3697
+  //  144   4096 x 24576 x  6144   443   409   390   377   377
+  p.band = static_cast<long long>(p.N) * p.K <= (32 << 20) ? 2 : 16;
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   if (tiles > INT_MAX / 2) return fail(SOL_ATTN_ERR_UNSUPPORTED, "%lld output tiles", tiles);
   CUtensorMap ma, mw, mo{};

@@ -342,3 +342,14 @@ def test_the_longest_sums_of_large_products():
     a, w = rows(M, K, 0, full=True), rows(N, K, 0, full=True)
     one = torch.ones(N, device="cuda")
     assert (sa.int8_linear(a, one[:M], w, one, out_dtype=FP32) == float(128 * 128 * K)).all()
+
+
+@pytest.mark.gpu
+def test_bands_of_tokens():
+    """Many tokens and few weights, which go through narrow bands: the last band is half full."""
+    M, N, K = 40_500, 777, 1000
+    a, w = rows(M, K, 58), rows(N, K, 59)
+    s, t = scales(M, 60, 0.01), scales(N, 61, 0.01 / math.sqrt(K))
+    out = sa.int8_linear(a, s, w, t)
+    check(out, a, s, w, t, None)
+    assert torch.equal(sa.int8_linear(a[-300:], s[-300:], w, t), out[-300:])
