@@ -11,11 +11,13 @@
 // and write the output; two accumulators alternate, so that one tile's output
 // is written while the next one's products run.
 //
-// Measured (B200): 75600 x 15360 x 5120 with bf16 output 3.64 to 3.80 ms, 3.13
-// to 3.27 POP/s, twice the measured bf16 rate of 1.63; back to back for seconds
-// 4.36 ms, as the power limit lowers the clock.  16384 x 5120 x 5120 270 us.
-// Shorter K (16384 x 1024 x 1024: 20 us for 10.5) is bound by what the tiles
-// bring from L2, 64 KB of operands for 128 x 256 x 128 products of an SM.
+// Measured (B200): 75600 x 15360 x 5120 with bf16 output 4.31 to 4.51 ms back to
+// back for seconds, 2.64 to 2.76 POP/s, where the power limit lowers the clock
+// (twice the measured sustained bf16 rate is 2.77); with pauses between calls 3.64
+// to 3.80 ms, 3.13 to 3.27 POP/s (twice the burst rate is 3.26).  16384 x 5120 x
+// 5120 270 us.  Shorter K (16384 x 1024 x 1024: 20 to 23 us for 10.5) has 256 tiles
+// for 74 pairs, 3.5 waves that take four, and eight steps a tile, in each of which
+// an SM is brought 32 KB of operands from L2.
 #pragma once
 
 #include "rows.cuh"
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // The weights are read once and each of their bytes meets MT tokens: bound by
 // their bytes, so plain 16-byte loads and dp4a.  A warp takes R channels, its
 // lanes 16 bytes each of K a step; where there are few channels the block's
-// warps share them and split K.  2 x 30720 x 5120: 26.7 us (24.0 at the copy
+// warps share them and split K.  2 x 30720 x 5120: 28.6 us (24.0 at the copy
 // rate); 1 x 5120 x 5120 5.8 us (4.0); 4 x 15360 x 5120 16.1 us, the MMA form
 // below 13.3, but 8.8 against 8.3 at 5120 channels and 5.1 against 4.1 at 256.
 constexpr int kVecRows = 4;      // channels of a warp

@@ -17,8 +17,8 @@
 // 6.15 TB/s; 708 us at the copy rate of 6.56); 4173 x 2 tokens of 16 heads of
 // 64 with positions 24 us (15.6), where a team has two or three tokens and the
 // first ones' latency is not hidden.  What brought it there from 1208 us: loads
-// through a ring instead of registers, tables and weights in shared memory
-// without bank conflicts, one barrier a token, no division in the loop.
+// through shared memory instead of registers, tables and weights there without
+// bank conflicts, one barrier a token, no division in the loop.
 #pragma once
 
 #include <climits>
@@ -58,8 +58,8 @@ struct RopeParams {
   int by_lanes;         // a head's items lie in lanes of one warp
   int packed;           // a token's heads lie one after the other in q, k and v
   int shared_weights;   // the weights are read from shared memory
-  int staged;           // tensors that go through the ring: q, k and, where there is room, v
-  int depth;            // stages of the ring
+  int staged;           // tensors that go through the stages: q, k and, where there is room, v
+  int depth;            // stages of a team: 1 to 4
   float inv_channels;   // 1 / channels of a norm
   double turns[kRopeMaxD / 2];        // frequency of a pair / (2 pi)
   unsigned char axis[kRopeMaxD / 2];  // axis of a pair
@@ -107,11 +107,14 @@ __device__ __forceinline__ void rope_turn(float (&a)[8], const float4& cs, const
 // One team to a token, all its heads.  An item is what turns together: a
 // vector of 8 channels (interleaved) or two that lie d / 2 channels apart
 // (half); each warp has 32 N consecutive items, each thread N of them.  Tokens
-// come through a ring of p.depth stages in shared memory by asynchronous
-// copies, each warp's part by that warp, and are read from there twice, for
-// the norm and for the rotation.  The cosines and sines of a token are made by
-// the team's first threads; their buffers alternate, so that the barrier of
-// the norm's sum is the only one.
+// come through p.depth stages in shared memory by asynchronous copies, each
+// warp's part by that warp, and are read from there twice, for the norm and for
+// the rotation.  The launch takes as many teams as fit and gives the stages what
+// is left.  With v that is one stage up to 40 heads of 128: a team asks for its
+// next token when it has read the present one, and the other teams' loads fill
+// the time; without v it is two in most of the 16-bit cases.  The cosines and
+// sines of a token are made by the team's first threads; their buffers alternate,
+// so that the barrier of the norm's sum is the only one.
 template <typename T, bool HALF, int WARPS>
 __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int VECS = HALF ? 2 : 1, N = kRopeVectors / VECS;
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_kernel(const __grid_cons
   const int nweights = p.norm == kRopeNormNone ? 0 : p.norm == kRopeNormToken ? p.H * p.d : p.d;
   const int tensors = p.staged;
   // shared memory: weights of q and k as two planes each (the first and the
-  // last four channels of each vector), the teams' tables and sums, the rings
+  // last four channels of each vector), the teams' tables and sums, the stages
   const int nshared = p.shared_weights ? 2 * nweights : 0;
   float* weights = smem;
   float* table0 = smem + nshared + team.index * 2 * p.team_floats;

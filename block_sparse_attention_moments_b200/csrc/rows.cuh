@@ -77,10 +77,9 @@ __device__ __forceinline__ void load_raw(Raw<T, 1>& v, const T* p) {
   v.r = *p;
 }
 
-// A warp's asynchronous copy of 32 consecutive vectors of 8 elements (those of
-// lanes with on[i]) into its own shared memory, and their way out of it.  The
-// copies go by 16-byte pieces in address order; a lane of fp32 finds its 32
-// bytes in pieces that two other lanes have copied, so it reads behind a
+// Asynchronous copies of 16 bytes into shared memory.  The kernels' warps bring
+// vectors of 8 elements by such pieces in address order; a lane of fp32 finds its
+// 32 bytes in pieces that two other lanes have copied, so it reads behind a
 // __syncwarp and the warp refills behind another.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

@@ -215,8 +215,8 @@ def norm_modulate(x, scale=None, shift=None, *, norm="layer", weight=None, bias=
                   quantize=False, out=None):
     """norm(x) * (1 + scale) + shift, token by token.
 
-    x: [B, L, C] or [L, C], bf16, fp16 or fp32, channels contiguous, any row strides.  norm: "layer", "rms" or
-    "none", over the C channels, then weight and bias [C].  scale, shift: [C], [B, C] or [B, G, C], each group for
+    x: [B, L, C] or [L, C], bf16, fp16 or fp32, C up to 16384, channels contiguous, any row strides.  norm: "layer",
+    "rms" or "none", over the C channels, then weight and bias [C].  scale, shift: [C], [B, C] or [B, G, C], each group for
     L / G consecutive tokens (frames, or G = L: every token its own); a first dimension of 1 serves every batch
     element.  Vectors may have any of the three types.  Returns h in x's type (out_dtype: another one, where x is
     fp32), or with quantize=True (q, s): int8 [B, L, C] and fp32 [B, L] with h ~ q * s[..., None], the rows of q

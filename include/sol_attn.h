@@ -352,7 +352,8 @@ int sol_attn_quantized_linear(const sol_attn_linear_args* args, void* stream);
  * returns SOL_ATTN_OK, or SOL_ATTN_ERR_TIMEOUT if a bounded wait of a product
  * gave up, whose output is then not valid, or SOL_ATTN_ERR_DEVICE if one refused
  * to run.  It tells of every product enqueued on stream before, and of others on
- * the device that have ended; a report is given once.  SOL_ATTN_ERR_STATE on a
+ * the device that have ended; a report is given once.  It takes four bytes of the
+ * device's memory pool meanwhile, in the stream's order.  SOL_ATTN_ERR_STATE on a
  * stream that is being captured. */
 int sol_attn_linear_status(void* stream);
 
