@@ -360,3 +360,40 @@ def test_layer_without_tokens(B, L):
     layer = sa.AttentionLayer(w["w_qkv"], w["w_out"], 2)
     xn, h = layer(torch.empty(B, L, 128, device="cuda"), beta=1.0, chunk=4, grid=(1, 1, 1))
     assert xn.shape == h.shape == (B, L, 128) and xn.dtype == FP32 and h.dtype == BF16
+
+
+@pytest.mark.gpu
+def test_host_threads_on_streams_of_their_own():
+    """The operators called by several threads at once, each on its stream: the bits of one thread's calls."""
+    import threading
+
+    def calls(x, w, ws):
+        a, s = sa.norm_modulate(x, quantize=True)
+        y = sa.int8_linear(a, s, w, ws)
+        q, k = sa.rope(y.view(2, -1, 3, 2, 64)[:, :, 0], y.view(2, -1, 3, 2, 64)[:, :, 1], grid=(2, 5, 30), norm="token")
+        return (y, q, k, *sa.gate_residual_norm(y, y, quantize=True))
+
+    inputs = []
+    for i, L in enumerate((1, 60, 300, 1000)):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        rnd = lambda *shape: torch.empty(shape, device="cuda").normal_(generator=g)
+        inputs.append((rnd(2, L, 128).to(BF16), *sa.quantize_rows(rnd(384, 128))))
+    want = [calls(*t) for t in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = calls(*inputs[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    sa.linear_status("cuda")
